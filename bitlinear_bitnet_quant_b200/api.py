@@ -12,6 +12,7 @@ import ctypes
 import glob
 import os
 import re
+from typing import NamedTuple
 
 import torch
 
@@ -66,6 +67,16 @@ _SIGNATURES = {
                                           ctypes.c_int, ctypes.c_double, _c_void_p, _c_void_p, _i64, _c_void_p]),
     "bitnet_attention": (ctypes.c_int, [_c_void_p, _c_void_p, _c_void_p, _i64, _i64, _i64, ctypes.c_int,
                                         ctypes.c_int, _i64, _c_void_p, _c_void_p]),
+    "bitnet_qk_norm_rope_append": (ctypes.c_int, [_c_void_p] * 3 + [ctypes.c_int] + [_i64] * 6 + [_c_void_p] * 2 +
+                                   [ctypes.c_int] * 3 + [_c_void_p] * 2 + [ctypes.c_float, ctypes.c_int, ctypes.c_double] +
+                                   [_c_void_p] * 3 + [_i64, _c_void_p]),
+    "bitnet_kv4_append": (ctypes.c_int, [_c_void_p] * 3 + [ctypes.c_int] + [_i64] * 6 + [_c_void_p] * 2 +
+                          [ctypes.c_int] * 3 + [_c_void_p] * 2 + [ctypes.c_float, ctypes.c_int, ctypes.c_double, ctypes.c_int] +
+                          [_c_void_p, ctypes.c_int] + [_c_void_p] * 4 + [_i64, _c_void_p]),
+    "bitnet_kv4_read": (ctypes.c_int, [_c_void_p] * 4 + [_i64] * 3 + [_c_void_p] * 2 + [ctypes.c_int] * 2 + [_i64] +
+                        [_c_void_p] * 2 + [ctypes.c_int, _c_void_p]),
+    "bitnet_kv4_attention": (ctypes.c_int, [_c_void_p, ctypes.c_int] + [_c_void_p] * 4 + [_i64] * 3 + [_c_void_p] * 2 +
+                             [ctypes.c_int] * 3 + [_i64] * 4 + [_c_void_p] * 2),
     "bitnet_device_error": (ctypes.c_int, [ctypes.POINTER(ctypes.c_int)]),
     "bitnet_measure_i8_mma": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, _c_void_p, _c_void_p,
                                              _c_void_p]),
@@ -350,6 +361,220 @@ def bitnet_attention(Q: torch.Tensor, Kc: torch.Tensor, Vc: torch.Tensor, B: int
     d = Q.shape[1] // heads
     _check("bitnet_attention", lib().bitnet_attention(
         _ptr(Q), _ptr(Kc), _ptr(Vc), B, L, t0, heads, d, Kc.shape[1], _ptr(A), _stream(stream)))
+    return A
+
+
+# The calls around a key/value step (norms, shared key heads, ragged steps, the
+# 4-bit cache).  They check shapes, types and devices here, run on the tensors'
+# device whichever is current, and allocate what is not passed in on the call's
+# stream.
+
+class KV4Cache(NamedTuple):
+    """A key/value cache held in 4 bits: codes uint8 [B, kv_heads, T_cap, d/2] and
+    steps fp32 [B, kv_heads, T_cap], of the keys and of the values."""
+    kc: torch.Tensor
+    ks: torch.Tensor
+    vc: torch.Tensor
+    vs: torch.Tensor
+
+
+def bitnet_kv4_cache(B: int, T_cap: int, kv_heads: int, head_dim: int = 128, device="cuda") -> KV4Cache:
+    """An empty (zeroed) 4-bit cache; T_cap is rounded up to a multiple of 16."""
+    T = -(-T_cap // 16) * 16
+    codes = lambda: torch.zeros((B, kv_heads, T, head_dim // 2), dtype=torch.uint8, device=device)
+    steps = lambda: torch.zeros((B, kv_heads, T), dtype=torch.float32, device=device)
+    return KV4Cache(codes(), steps(), codes(), steps())
+
+
+def _expect(t: torch.Tensor, name: str, dtype, shape, device):
+    """t is a contiguous tensor of this type and shape on this CUDA device."""
+    if not (t.is_cuda and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+
+
+def _row_stride(t: torch.Tensor, name: str, rows: int, width: int, like: torch.Tensor) -> int:
+    """Row stride, in values, of t [rows, width] with contiguous rows (a view of a wider tensor is fine)."""
+    if not (t.is_cuda and t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1)):
+        raise ValueError(f"{name} must be a CUDA tensor of contiguous rows")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype}, not {t.dtype}")
+    if t.shape[0] != rows or t.shape[1] != width:
+        raise ValueError(f"{name} must have shape {(rows, width)}, not {tuple(t.shape)}")
+    return t.stride(0) if rows > 1 else width
+
+
+def _step_args(pos, lens, B: int, device):
+    for t, n in ((pos, "pos"), (lens, "lens")):
+        if t is not None:
+            _expect(t, n, torch.int32, (B,), device)
+    return _ptr(pos), _ptr(lens)
+
+
+def _cache_dims(cache: KV4Cache, B: int, device):
+    """(kv_heads, T_cap, d) of a 4-bit cache, checked."""
+    if cache.kc.dim() != 4:
+        raise ValueError("a 4-bit cache's codes are [B, kv_heads, T_cap, d/2]")
+    _, kv, T, half = cache.kc.shape
+    for t, n in ((cache.kc, "cache.kc"), (cache.vc, "cache.vc")):
+        _expect(t, n, torch.uint8, (B, kv, T, half), device)
+    for t, n in ((cache.ks, "cache.ks"), (cache.vs, "cache.vs")):
+        _expect(t, n, torch.float32, (B, kv, T), device)
+    return kv, T, 2 * half
+
+
+class _On:
+    """Makes `device` current for the call; `stream` is the call's stream there."""
+
+    def __init__(self, device, stream):
+        self.stream = torch.cuda.current_stream(device) if stream is None else stream
+        self.ptr = ctypes.c_void_p(self.stream.cuda_stream)
+        self.guard = torch.cuda.device(device) if device.index != torch.cuda.current_device() else None
+        self.given = stream is not None
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    def empty(self, shape, dtype, device):
+        """Memory that belongs to the call's stream."""
+        if not self.given:
+            return torch.empty(shape, dtype=dtype, device=device)
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _append_rows(Q, K, V, B, L, heads, kv_heads, d, gamma_q, gamma_k):
+    rows, dev = B * L, Q.device
+    ld = (_row_stride(Q, "Q", rows, heads * d, Q), _row_stride(K, "K", rows, kv_heads * d, Q),
+          _row_stride(V, "V", rows, kv_heads * d, Q))
+    for t, n in ((gamma_q, "gamma_q"), (gamma_k, "gamma_k")):
+        if t is not None:
+            _expect(t, n, torch.float32, (d,), dev)
+    return ld
+
+
+def bitnet_qk_norm_rope_append(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, Kc: torch.Tensor, Vc: torch.Tensor,
+                               B: int, L: int, t0: int, heads: int, kv_heads: int | None = None, gamma_q=None,
+                               gamma_k=None, eps: float = 1e-6, rot_dim: int | None = None, base: float = 10000.0,
+                               pos=None, lens=None, Qo=None, stream=None):
+    """bitnet_rope_append with RMSNorm of every query and key head in the same pass:
+    Q [B*L, heads*d], K, V [B*L, kv_heads*d] fp32 or bf16 (row-strided views are
+    fine); Kc, Vc fp32 [B, T_cap, kv_heads*d].  Token l of sequence b sits at
+    position t0 + pos[b] + l; only the first lens[b] tokens are real.  Returns the
+    turned queries Qo, fp32 [B*L, heads*d] (pass Q itself, fp32, to turn in place)."""
+    kv_heads = heads if kv_heads is None else kv_heads
+    dev = Q.device
+    _require(Kc, "Kc")
+    T, d = Kc.shape[1], Kc.shape[2] // kv_heads
+    rot_dim = d if rot_dim is None else rot_dim
+    ldq, ldk, ldv = _append_rows(Q, K, V, B, L, heads, kv_heads, d, gamma_q, gamma_k)
+    for t, n in ((Kc, "Kc"), (Vc, "Vc")):
+        _expect(t, n, torch.float32, (B, T, kv_heads * d), dev)
+    p, ln = _step_args(pos, lens, B, dev)
+    with _On(dev, stream) as on:
+        if Qo is None:
+            Qo = on.empty((B * L, heads * d), torch.float32, dev)
+        _expect(Qo, "Qo", torch.float32, (B * L, heads * d), dev)
+        _check("bitnet_qk_norm_rope_append", lib().bitnet_qk_norm_rope_append(
+            _ptr(Q), _ptr(K), _ptr(V), _dtype_code(Q), ldq, ldk, ldv, B, L, t0, p, ln, heads, kv_heads, d,
+            _ptr(gamma_q), _ptr(gamma_k), float(eps), int(rot_dim), float(base), _ptr(Qo), _ptr(Kc), _ptr(Vc), T,
+            on.ptr))
+    return Qo
+
+
+def bitnet_kv4_append(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cache: KV4Cache, B: int, L: int, t0: int,
+                      heads: int, norm: bool = False, gamma_q=None, gamma_k=None, eps: float = 1e-6,
+                      hadamard: bool = False, rot_dim: int | None = None, base: float = 10000.0, pos=None, lens=None,
+                      Qo=None, stream=None):
+    """Norm (optional), rotation and Hadamard (optional) of the query and key heads,
+    and the append of keys and values to a 4-bit cache.  Rows as for
+    bitnet_qk_norm_rope_append.  Returns the turned queries Qo [B*L, heads*d], in Q's
+    type unless passed in (fp32 or bf16; Q itself turns in place)."""
+    dev = Q.device
+    if not Q.is_cuda:
+        raise ValueError("Q must be a CUDA tensor of contiguous rows")
+    kv, T, d = _cache_dims(cache, B, dev)
+    rot_dim = d if rot_dim is None else rot_dim
+    ldq, ldk, ldv = _append_rows(Q, K, V, B, L, heads, kv, d, gamma_q, gamma_k)
+    p, ln = _step_args(pos, lens, B, dev)
+    flags = (1 if norm else 0) | (2 if hadamard else 0)
+    with _On(dev, stream) as on:
+        if Qo is None:
+            Qo = on.empty((B * L, heads * d), Q.dtype, dev)
+        _expect(Qo, "Qo", Qo.dtype, (B * L, heads * d), dev)
+        _check("bitnet_kv4_append", lib().bitnet_kv4_append(
+            _ptr(Q), _ptr(K), _ptr(V), _dtype_code(Q), ldq, ldk, ldv, B, L, t0, p, ln, heads, kv, d, _ptr(gamma_q),
+            _ptr(gamma_k), float(eps), int(rot_dim), float(base), flags, _ptr(Qo), _dtype_code(Qo), _ptr(cache.kc),
+            _ptr(cache.ks), _ptr(cache.vc), _ptr(cache.vs), T, on.ptr))
+    return Qo
+
+
+def bitnet_kv4_read(cache: KV4Cache, B: int, L: int, t0: int, pos=None, lens=None, dtype=torch.float32, K=None, V=None,
+                    stream=None):
+    """The values a 4-bit cache holds for the tokens of a step: (K, V), each
+    [B*L, kv_heads*d] in `dtype` (or the type of the tensors passed in).  Rows of
+    padding and of positions outside the cache are left as they were (zeros where the
+    tensors are allocated here)."""
+    dev = cache.kc.device
+    kv, T, d = _cache_dims(cache, B, dev)
+    p, ln = _step_args(pos, lens, B, dev)
+    with _On(dev, stream) as on:
+        dtype = K.dtype if K is not None else V.dtype if V is not None else dtype
+        fresh = lambda: on.empty((B * L, kv * d), dtype, dev)
+        K_new, V_new = K is None, V is None
+        K, V = (fresh() if K_new else K), (fresh() if V_new else V)
+        for t, n in ((K, "K"), (V, "V")):
+            _expect(t, n, dtype, (B * L, kv * d), dev)
+        if (K_new or V_new) and (pos is not None or lens is not None):
+            with torch.cuda.stream(on.stream):
+                if K_new:
+                    K.zero_()
+                if V_new:
+                    V.zero_()
+        _check("bitnet_kv4_read", lib().bitnet_kv4_read(
+            _ptr(cache.kc), _ptr(cache.ks), _ptr(cache.vc), _ptr(cache.vs), B, L, t0, p, ln, kv, d, T, _ptr(K), _ptr(V),
+            _dtype_code(K), on.ptr))
+    return K, V
+
+
+def bitnet_kv4_attention(Q: torch.Tensor, cache: KV4Cache, B: int, L: int, t0: int, heads: int, window: int = 0,
+                         sinks: int = 0, t_max: int | None = None, pos=None, lens=None, A=None, stream=None):
+    """Causal softmax attention of the rows Q [B*L, heads*d] (fp32 or bf16) over a
+    4-bit cache; with window > 0 over the last `window` keys and the first `sinks`.
+    t_max: a bound on the positions in use plus one, for the split of the work over
+    the GPU (default: t0 + L without pos, else T_cap).  Returns A in Q's type; rows
+    of padding are left as they were (zeros where A is allocated here)."""
+    dev = Q.device
+    if not Q.is_cuda:
+        raise ValueError("Q must be a contiguous CUDA tensor")
+    kv, T, d = _cache_dims(cache, B, dev)
+    _expect(Q, "Q", Q.dtype, (B * L, heads * d), dev)
+    p, ln = _step_args(pos, lens, B, dev)
+    if t_max is None:
+        t_max = t0 + L if pos is None else T
+    with _On(dev, stream) as on:
+        if A is None:
+            A = on.empty((B * L, heads * d), Q.dtype, dev)
+            if lens is not None:
+                with torch.cuda.stream(on.stream):
+                    A.zero_()
+        _expect(A, "A", Q.dtype, (B * L, heads * d), dev)
+        _check("bitnet_kv4_attention", lib().bitnet_kv4_attention(
+            _ptr(Q), _dtype_code(Q), _ptr(cache.kc), _ptr(cache.ks), _ptr(cache.vc), _ptr(cache.vs), B, L, t0, p, ln,
+            heads, kv, d, T, int(window), int(sinks), min(int(t_max), T), _ptr(A), on.ptr))
     return A
 
 

@@ -46,7 +46,16 @@ class BitLinearChain:
     sequences of L tokens each; every layer keeps a key/value cache
     [B, T_cap, hidden] (allocated here) and runs rotary embedding, the cache
     append and causal softmax attention; forward(x, t0) places the step's
-    tokens at positions t0 .. t0+L-1."""
+    tokens at positions t0 .. t0+L-1.  More keys of the dict:
+      kv_bits    32 (default) or 4: the caches are then held in 4 bits (kv4, one
+                 api.KV4Cache a layer) and read by the attention as they are;
+      qk_norm    RMSNorm of every query and key head before the rotation, with
+                 gamma_q / gamma_k ([d] fp32 a layer, a list) or ones;
+      hadamard   (kv_bits 4; default True) Hadamard transform of the query and
+                 key heads before the keys are held in 4 bits;
+      kv_heads   (kv_bits 4; default heads) key heads, each shared by
+                 heads / kv_heads query heads;
+      window, sinks  (kv_bits 4) sliding window and first tokens that stay visible."""
 
     def __init__(self, layers: list, M: int, hidden: int, ffn: int, device, eps: float = 1e-6, attention=None):
         self.layers = layers
@@ -57,16 +66,33 @@ class BitLinearChain:
             assert B * L == M and L <= T_cap
             self.heads = attention.get("heads", 16)
             self.rope_base = attention.get("base", 10000.0)
-            self.kc = [torch.empty((B, T_cap, hidden), dtype=torch.float32, device=device) for _ in layers]
-            self.vc = [torch.empty((B, T_cap, hidden), dtype=torch.float32, device=device) for _ in layers]
-            self.att = torch.empty((M, hidden), dtype=torch.float32, device=device)
+            self.kv_bits = attention.get("kv_bits", 32)
+            self.kv_heads = attention.get("kv_heads", self.heads)
+            self.qk_norm = attention.get("qk_norm", False)
+            self.gamma_q, self.gamma_k = (attention.get(g) or [None] * len(layers) for g in ("gamma_q", "gamma_k"))
+            self.hadamard = attention.get("hadamard", True)
+            self.window, self.sinks = attention.get("window", 0), attention.get("sinks", 0)
+            if self.kv_bits == 4:
+                self.kv4 = [api.bitnet_kv4_cache(B, T_cap, self.kv_heads, hidden // self.heads, device) for _ in layers]
+                self.att = torch.zeros((M, hidden), dtype=torch.float32, device=device)
+            elif self.kv_bits == 32:
+                if self.kv_heads != self.heads or self.window or self.sinks:
+                    raise ValueError("shared key heads and a sliding window need kv_bits=4")
+                self.kc = [torch.empty((B, T_cap, hidden), dtype=torch.float32, device=device) for _ in layers]
+                self.vc = [torch.empty((B, T_cap, hidden), dtype=torch.float32, device=device) for _ in layers]
+                self.att = torch.empty((M, hidden), dtype=torch.float32, device=device)
+            else:
+                raise ValueError("kv_bits is 32 or 4")
         self.t0 = 0
+        self.pos = self.lens = None
         f32 = dict(dtype=torch.float32, device=device)
         e = lambda *shape: torch.empty(shape, **f32)
         self.x = [e(M, hidden), e(M, hidden)]          # layer input, chain output
         self.xq = torch.empty((M, hidden), dtype=torch.int8, device=device)
         self.sx = e(M)
-        self.q, self.k, self.v, self.o, self.h, self.d = (e(M, hidden) for _ in range(6))
+        self.q, self.o, self.h, self.d = (e(M, hidden) for _ in range(4))
+        kv_width = hidden if attention is None else hidden // self.heads * self.kv_heads
+        self.k, self.v = e(M, kv_width), e(M, kv_width)
         self.v4 = torch.empty((M, hidden // 2), dtype=torch.uint8, device=device)
         self.sv = e(M)
         self.hq = torch.empty((M, hidden), dtype=torch.int8, device=device)
@@ -91,11 +117,7 @@ class BitLinearChain:
         if self.attention is None:
             att = self.v                                   # a one-token context returns V
         else:
-            B, L = self.attention["B"], self.attention["L"]
-            A.bitnet_rope_append(self.q, self.k, self.v, self.kc[index], self.vc[index], B, L, self.t0, self.heads,
-                                 self.rope_base, stream=s)
-            att = A.bitnet_attention(self.q, self.kc[index], self.vc[index], B, L, self.t0, self.heads, A=self.att,
-                                     stream=s)
+            att = self.attend(index, s)
         A.bitnet_hadamard_quant_act(att, None, self.eps, 0, Xq4=self.v4, s_x=self.sv, stream=s)
         A.bitnet_linear(self.v4, 4, self.sv, *w["o"], Y=self.o, stream=s)
         A.bitnet_add_quant_act(x, self.o, None, self.eps, H=self.h, Xq=self.hq, s_x=self.sh, stream=s)
@@ -104,11 +126,36 @@ class BitLinearChain:
         A.bitnet_linear(self.a4, 4, self.sa, *w["down"], Y=self.d, stream=s)
         return self.h, self.d
 
-    def forward(self, x: torch.Tensor, stream=None, t0: int = 0) -> torch.Tensor:
+    def attend(self, index: int, stream=None):
+        """Rotation (and norm), cache append and attention of layer `index`, from
+        the projections in q, k, v."""
+        A, s = api, stream
+        B, L = self.attention["B"], self.attention["L"]
+        norm = dict(gamma_q=self.gamma_q[index], gamma_k=self.gamma_k[index], eps=self.eps, base=self.rope_base)
+        if self.kv_bits == 4:
+            at = dict(pos=self.pos, lens=self.lens, stream=s)
+            A.bitnet_kv4_append(self.q, self.k, self.v, self.kv4[index], B, L, self.t0, self.heads, norm=self.qk_norm,
+                                hadamard=self.hadamard, Qo=self.q, **norm, **at)
+            return A.bitnet_kv4_attention(self.q, self.kv4[index], B, L, self.t0, self.heads, self.window, self.sinks,
+                                          A=self.att, **at)
+        if self.qk_norm:
+            A.bitnet_qk_norm_rope_append(self.q, self.k, self.v, self.kc[index], self.vc[index], B, L, self.t0,
+                                         self.heads, Qo=self.q, stream=s, **norm)
+        else:
+            A.bitnet_rope_append(self.q, self.k, self.v, self.kc[index], self.vc[index], B, L, self.t0, self.heads,
+                                 self.rope_base, stream=s)
+        return A.bitnet_attention(self.q, self.kc[index], self.vc[index], B, L, self.t0, self.heads, A=self.att,
+                                  stream=s)
+
+    def forward(self, x: torch.Tensor, stream=None, t0: int = 0, pos=None, lens=None) -> torch.Tensor:
         """x: [M, hidden] fp32 on the device; returns the last layer's output
         (one of the chain's own buffers).  t0: position of each sequence's first
-        token in this step (with attention)."""
-        self.t0 = t0
+        token in this step (with attention).  With kv_bits 4, pos and lens ([B] int32
+        on the device) place each sequence's tokens at t0 + pos[b] on and mark the rows
+        behind its first lens[b] as padding; a captured forward reads them at replay."""
+        if (pos is not None or lens is not None) and (self.attention is None or self.kv_bits != 4):
+            raise ValueError("pos and lens need attention with kv_bits=4")
+        self.t0, self.pos, self.lens = t0, pos, lens
         parts = (x,)
         for i, w in enumerate(self.layers):
             parts = self.layer(parts, w, stream, i)

@@ -7,6 +7,7 @@
 
 #include "../../include/bitnet.h"
 #include "common.cuh"
+#include "kv4_common.cuh"
 
 namespace bitnet {
 __device__ int g_device_error = 0;
@@ -43,6 +44,10 @@ cudaError_t run_rope_append(float* Q, const float* K, const float* V, int B, int
                             double base, float* Kc, float* Vc, int T_cap, cudaStream_t st);
 cudaError_t run_attention(const float* Q, const float* Kc, const float* Vc, int B, int L, int t0, int heads, int d,
                           int T_cap, float* A, cudaStream_t st);
+cudaError_t run_append(const KvStep& s, const AppendArgs& a, int x_bf16, int d, double base, cudaStream_t st);
+cudaError_t run_kv4_read(const KvStep& s, int kv_heads, int d, const uint8_t* Kc, const float* Ks, const uint8_t* Vc,
+                         const float* Vs, void* K, void* V, int bf16, cudaStream_t st);
+cudaError_t run_kv4_attention(const KvStep& s, const AttnArgs& a, int bf16, int d, int64_t t_max, cudaStream_t st);
 }  // namespace bitnet
 
 namespace {
@@ -380,6 +385,176 @@ int bitnet_attention(const float* Q, const float* Kc, const float* Vc, int64_t B
   if (d != BITNET_OK) return d;
   return cuda_status(bitnet::run_attention(Q, Kc, Vc, (int)B, (int)L, (int)t0, heads, head_dim, (int)T_cap, A,
                                            static_cast<cudaStream_t>(stream)));
+}
+
+// Limits that the calls around a key/value step share.
+static int kv_shape(int64_t B, int64_t L, int64_t t0, const int32_t* pos, int heads, int kv_heads, int head_dim,
+                    int64_t T_cap) {
+  if (head_dim != 64 && head_dim != 128) return BITNET_ERR_SHAPE;
+  if (heads < 1 || heads > 256 || kv_heads < 1 || heads % kv_heads != 0) return BITNET_ERR_SHAPE;
+  if (B < 0 || B > 65535 || L < 0 || L >= (int64_t(1) << 31) || B * L * heads >= (int64_t(1) << 31))
+    return BITNET_ERR_SHAPE;
+  if (T_cap < 1 || T_cap > (int64_t(1) << 24) || t0 < 0 || t0 > (int64_t(1) << 24)) return BITNET_ERR_SHAPE;
+  if (!pos && t0 + L > T_cap) return BITNET_ERR_SHAPE;
+  if (B * T_cap * kv_heads * head_dim >= (int64_t(1) << 40)) return BITNET_ERR_SHAPE;
+  return BITNET_OK;
+}
+
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+static bitnet::KvStep kv_step(int64_t B, int64_t L, int64_t t0, const int32_t* pos, const int32_t* len,
+                              int64_t T_cap) {
+  bitnet::KvStep s = {};
+  s.pos = pos;
+  s.len = len;
+  s.t0 = t0;
+  s.B = (int)B;
+  s.L = (int)L;
+  s.T_cap = (int)T_cap;
+  return s;
+}
+
+// The rows, factors and sizes of an append; the caches are checked by the callers.
+static int append_check(const void* Q, const void* K, const void* V, int x_dtype, int64_t ldq, int64_t ldk,
+                        int64_t ldv, const int32_t* pos, const int32_t* len, int heads, int kv_heads, int head_dim,
+                        const float* gamma_q, const float* gamma_k, int rot_dim, double base, const void* Qo,
+                        int q_dtype) {
+  if (x_dtype != BITNET_F32 && x_dtype != BITNET_BF16) return BITNET_ERR_DTYPE;
+  if (q_dtype != BITNET_F32 && q_dtype != BITNET_BF16) return BITNET_ERR_DTYPE;
+  if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 2 != 0) return BITNET_ERR_SHAPE;
+  if (!(base > 1.0) || !(base < 1e300)) return BITNET_ERR_SHAPE;
+  const int64_t wq = (int64_t)heads * head_dim, wk = (int64_t)kv_heads * head_dim, most = int64_t(1) << 31;
+  if (ldq < wq || ldk < wk || ldv < wk || ldq >= most || ldk >= most || ldv >= most) return BITNET_ERR_SHAPE;
+  if (!Q || !K || !V || !Qo) return BITNET_ERR_NULL;
+  if (Qo == Q && (q_dtype != x_dtype || ldq != wq)) return BITNET_ERR_SHAPE;
+  const int64_t per16 = x_dtype == BITNET_F32 ? 4 : 8;
+  if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(Qo) || ldq % per16 || ldk % per16 ||
+      ldv % per16 || (gamma_q && !aligned16(gamma_q)) || (gamma_k && !aligned16(gamma_k)) || !aligned4(pos) ||
+      !aligned4(len))
+    return BITNET_ERR_ALIGN;
+  return BITNET_OK;
+}
+
+static bitnet::AppendArgs append_args(const void* Q, const void* K, const void* V, int64_t ldq, int64_t ldk,
+                                      int64_t ldv, int heads, int kv_heads, const float* gamma_q,
+                                      const float* gamma_k, float eps, int rot_dim, int flags, void* Qo,
+                                      int q_dtype) {
+  bitnet::AppendArgs a = {};
+  a.Q = Q;
+  a.K = K;
+  a.V = V;
+  a.ldq = ldq;
+  a.ldk = ldk;
+  a.ldv = ldv;
+  a.gamma_q = gamma_q;
+  a.gamma_k = gamma_k;
+  a.eps = eps;
+  a.heads = heads;
+  a.kv_heads = kv_heads;
+  a.rot_dim = rot_dim;
+  a.norm = (flags & BITNET_KV_NORM) != 0;
+  a.hadamard = (flags & BITNET_KV_HADAMARD) != 0;
+  a.Qo = Qo;
+  a.qo_bf16 = q_dtype == BITNET_BF16;
+  return a;
+}
+
+int bitnet_qk_norm_rope_append(const void* Q, const void* K, const void* V, int x_dtype, int64_t ldq, int64_t ldk,
+                               int64_t ldv, int64_t B, int64_t L, int64_t t0, const int32_t* pos, const int32_t* len,
+                               int heads, int kv_heads, int head_dim, const float* gamma_q, const float* gamma_k,
+                               float eps, int rot_dim, double base, float* Qo, float* Kc, float* Vc, int64_t T_cap,
+                               void* stream) {
+  const int sh = kv_shape(B, L, t0, pos, heads, kv_heads, head_dim, T_cap);
+  if (sh != BITNET_OK) return sh;
+  if (B == 0 || L == 0) return BITNET_OK;
+  const int c = append_check(Q, K, V, x_dtype, ldq, ldk, ldv, pos, len, heads, kv_heads, head_dim, gamma_q, gamma_k,
+                             rot_dim, base, Qo, BITNET_F32);
+  if (c != BITNET_OK) return c;
+  if (!Kc || !Vc) return BITNET_ERR_NULL;
+  if (!aligned16(Kc) || !aligned16(Vc)) return BITNET_ERR_ALIGN;
+  const int d = check_device();
+  if (d != BITNET_OK) return d;
+  bitnet::AppendArgs a = append_args(Q, K, V, ldq, ldk, ldv, heads, kv_heads, gamma_q, gamma_k, eps, rot_dim,
+                                     BITNET_KV_NORM, Qo, BITNET_F32);
+  a.Kc32 = Kc;
+  a.Vc32 = Vc;
+  return cuda_status(bitnet::run_append(kv_step(B, L, t0, pos, len, T_cap), a, x_dtype == BITNET_BF16, head_dim, base,
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+int bitnet_kv4_append(const void* Q, const void* K, const void* V, int x_dtype, int64_t ldq, int64_t ldk, int64_t ldv,
+                      int64_t B, int64_t L, int64_t t0, const int32_t* pos, const int32_t* len, int heads,
+                      int kv_heads, int head_dim, const float* gamma_q, const float* gamma_k, float eps, int rot_dim,
+                      double base, int flags, void* Qo, int q_dtype, uint8_t* Kc, float* Ks, uint8_t* Vc, float* Vs,
+                      int64_t T_cap, void* stream) {
+  const int sh = kv_shape(B, L, t0, pos, heads, kv_heads, head_dim, T_cap);
+  if (sh != BITNET_OK) return sh;
+  if (T_cap % 16 != 0 || (flags & ~(BITNET_KV_NORM | BITNET_KV_HADAMARD)) != 0) return BITNET_ERR_SHAPE;
+  if (B == 0 || L == 0) return BITNET_OK;
+  const int c = append_check(Q, K, V, x_dtype, ldq, ldk, ldv, pos, len, heads, kv_heads, head_dim, gamma_q, gamma_k,
+                             rot_dim, base, Qo, q_dtype);
+  if (c != BITNET_OK) return c;
+  if (!Kc || !Ks || !Vc || !Vs) return BITNET_ERR_NULL;
+  if (!aligned16(Kc) || !aligned16(Ks) || !aligned16(Vc) || !aligned16(Vs)) return BITNET_ERR_ALIGN;
+  const int d = check_device();
+  if (d != BITNET_OK) return d;
+  bitnet::AppendArgs a = append_args(Q, K, V, ldq, ldk, ldv, heads, kv_heads, gamma_q, gamma_k, eps, rot_dim, flags,
+                                     Qo, q_dtype);
+  a.Kc4 = Kc;
+  a.Ks = Ks;
+  a.Vc4 = Vc;
+  a.Vs = Vs;
+  return cuda_status(bitnet::run_append(kv_step(B, L, t0, pos, len, T_cap), a, x_dtype == BITNET_BF16, head_dim, base,
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+int bitnet_kv4_read(const uint8_t* Kc, const float* Ks, const uint8_t* Vc, const float* Vs, int64_t B, int64_t L,
+                    int64_t t0, const int32_t* pos, const int32_t* len, int kv_heads, int head_dim, int64_t T_cap,
+                    void* K, void* V, int dtype, void* stream) {
+  if (dtype != BITNET_F32 && dtype != BITNET_BF16) return BITNET_ERR_DTYPE;
+  const int sh = kv_shape(B, L, t0, pos, kv_heads, kv_heads, head_dim, T_cap);
+  if (sh != BITNET_OK) return sh;
+  if (T_cap % 16 != 0) return BITNET_ERR_SHAPE;
+  if (B == 0 || L == 0) return BITNET_OK;
+  if ((!K && !V) || (K && (!Kc || !Ks)) || (V && (!Vc || !Vs))) return BITNET_ERR_NULL;
+  if (!aligned16(Kc) || !aligned16(Ks) || !aligned16(Vc) || !aligned16(Vs) || !aligned16(K) || !aligned16(V) ||
+      !aligned4(pos) || !aligned4(len))
+    return BITNET_ERR_ALIGN;
+  const int d = check_device();
+  if (d != BITNET_OK) return d;
+  return cuda_status(bitnet::run_kv4_read(kv_step(B, L, t0, pos, len, T_cap), kv_heads, head_dim, Kc, Ks, Vc, Vs, K,
+                                          V, dtype == BITNET_BF16, static_cast<cudaStream_t>(stream)));
+}
+
+int bitnet_kv4_attention(const void* Q, int dtype, const uint8_t* Kc, const float* Ks, const uint8_t* Vc,
+                         const float* Vs, int64_t B, int64_t L, int64_t t0, const int32_t* pos, const int32_t* len,
+                         int heads, int kv_heads, int head_dim, int64_t T_cap, int64_t window, int64_t sinks,
+                         int64_t t_max, void* A, void* stream) {
+  if (dtype != BITNET_F32 && dtype != BITNET_BF16) return BITNET_ERR_DTYPE;
+  const int sh = kv_shape(B, L, t0, pos, heads, kv_heads, head_dim, T_cap);
+  if (sh != BITNET_OK) return sh;
+  if (T_cap % 16 != 0 || window < 0 || sinks < 0 || t_max < 0 || t_max > T_cap) return BITNET_ERR_SHAPE;
+  if (B == 0 || L == 0) return BITNET_OK;
+  if (!Q || !Kc || !Ks || !Vc || !Vs || !A) return BITNET_ERR_NULL;
+  if (!aligned16(Q) || !aligned16(Kc) || !aligned16(Ks) || !aligned16(Vc) || !aligned16(Vs) || !aligned16(A) ||
+      !aligned4(pos) || !aligned4(len))
+    return BITNET_ERR_ALIGN;
+  const int d = check_device();
+  if (d != BITNET_OK) return d;
+  const int64_t most = int64_t(1) << 25;                  // past every position
+  bitnet::AttnArgs a = {};
+  a.Q = Q;
+  a.Kc = Kc;
+  a.Ks = Ks;
+  a.Vc = Vc;
+  a.Vs = Vs;
+  a.A = A;
+  a.heads = heads;
+  a.kv_heads = kv_heads;
+  a.window = (int)(window < most ? window : most);
+  a.sinks = (int)(sinks < most ? sinks : most);
+  return cuda_status(bitnet::run_kv4_attention(kv_step(B, L, t0, pos, len, T_cap), a, dtype == BITNET_BF16, head_dim,
+                                               t_max > 0 ? t_max : T_cap, static_cast<cudaStream_t>(stream)));
 }
 
 int bitnet_device_error(int* code_out) {

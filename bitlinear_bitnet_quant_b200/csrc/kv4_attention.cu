@@ -1,0 +1,512 @@
+// Causal softmax attention over the 4-bit key/value cache, optionally through a
+// sliding window with a few first keys that stay visible.
+//
+//   score  s_j = (q . code_kj) step_kj / sqrt(d)
+//   output sum_j e^(s_j) step_vj code_vj / sum_j e^(s_j)
+//   over the keys j <= p with window == 0 or j > p - window or j < sinks.
+//
+// Codes are small integers, exact in fp16, so both products run on the tensor
+// cores with fp16 operands and fp32 sums:
+//   - q is scaled by a power of two for each row (its largest value then lies in
+//     [2^14, 2^15)); bf16 queries are then exact in fp16, fp32 queries are split into
+//     two fp16 terms (22 bits);
+//   - the value step is folded into the weight: with step_v = f 2^e the weight's
+//     exponent takes e, p'_j = 2^(s_j log2(e) + e_j - m), the operand is p'_j f_j in
+//     fp16 (two terms for fp32 outputs) and the sum takes p'_j 2^(-e_j).  The running
+//     maximum m is that of s_j log2(e) + e_j, so the operand's largest value is near
+//     2^10 whatever the steps' range, and what fp16 cannot hold is 2^-34 of it.
+// The softmax runs in one pass over the keys (running maximum and sum, fp32).
+#include "kv4_common.cuh"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+namespace bitnet {
+
+BN_DEV float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+BN_DEV uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// What the fp16 pair h leaves of (lo, hi), as another fp16 pair.
+BN_DEV uint32_t half2_rest(uint32_t h, float lo, float hi) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return pack_half2(lo - f.x, hi - f.y);
+}
+
+// A step's exponent e, at least -24: the append writes steps of 2^-20 and more (or a
+// row is empty, step 0, and keeps its weight in the sum).  Together with steps below
+// 2^60 no weight p' that counts leaves the range of fp32 (2^-126): 2^(-24 - 60) of
+// the largest one, times the weight itself.
+BN_DEV int step_exponent(float step) {
+  const int e = (int)((__float_as_uint(step) >> 23) & 255u) - 127;
+  return e < -24 ? -24 : (e > 126 ? 126 : e);
+}
+BN_DEV float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// The key tiles (of KT keys) that some query of positions p_lo .. p_hi sees: those
+// of the sinks, then those from the first query's window on.
+struct KeyTiles {
+  int sink_tiles, first, count;
+  BN_DEV int at(int i) const { return i < sink_tiles ? i : first + i - sink_tiles; }
+};
+template <int KT>
+BN_DEV KeyTiles key_tiles(int p_lo, int p_hi, int window, int sinks) {
+  KeyTiles k;
+  const int hi = p_hi + 1;
+  int lo = 0, sk = 0;
+  if (window > 0) {
+    lo = p_lo - window + 1 > 0 ? p_lo - window + 1 : 0;
+    sk = sinks < hi ? sinks : hi;
+  }
+  k.sink_tiles = (sk + KT - 1) / KT;
+  k.first = lo / KT > k.sink_tiles ? lo / KT : k.sink_tiles;
+  const int end = (hi + KT - 1) / KT;
+  k.count = k.sink_tiles + (end > k.first ? end - k.first : 0);
+  return k;
+}
+BN_DEV bool key_visible(int j, int p, int window, int sinks) {
+  return j <= p && (window == 0 || j > p - window || j < sinks);
+}
+
+// ---------------------------------------------------------------------------
+// few queries a key head: warp-level products (m16n8k16), keys as the 16 rows and
+// queries as the 8 columns, so that up to 8 queries (the heads that share a key
+// head, times a few tokens) cost one product.  A warp takes every (warps)-th tile
+// of 32 keys through its own ring of asynchronous copies; scores, weights and the
+// output stay in its registers.  The warps' partial softmaxes are merged in shared
+// memory, the blocks of a cluster over distributed shared memory.
+// ---------------------------------------------------------------------------
+constexpr int KD_WARPS = 4;
+constexpr int KD_STAGES = 4;
+constexpr int KD_KT = 32;                            // keys a tile
+
+template <int D>
+struct KdTile {                                      // one stage of a warp's ring, in bytes
+  static constexpr int CODES = KD_KT * D / 2;
+  static constexpr int BYTES = 2 * CODES + 2 * KD_KT * 4;
+};
+
+BN_DEV void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+BN_DEV uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+BN_DEV float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// A tile's codes and steps into one stage.  Keys past the cache's end are zero.
+// Value rows 2t of each 8 lie first, then rows 2t + 1: the product's lanes read rows
+// 2t (t = 0..3) at once, then without bank conflicts.
+template <int D>
+BN_DEV void kd_stage(const uint8_t* kc, const float* ks, const uint8_t* vc, const float* vs, int j0, int T_cap,
+                     uint8_t* stage, int lane) {
+  constexpr int CPR = D / 32;                        // 16-byte chunks a row
+  const uint32_t dst = smem_u32(stage);
+#pragma unroll
+  for (int i = 0; i < CPR; ++i) {
+    const int e = lane + 32 * i, r = e / CPR, c = e - r * CPR;
+    const bool in = j0 + r < T_cap;
+    const int64_t off = in ? (int64_t)(j0 + r) * (D / 2) + 16 * c : 0;
+    const int vr = (r & ~7) | ((r & 7) >> 1) | ((r & 1) << 2);
+    cp_async_16(dst + r * (D / 2) + 16 * c, kc + off, in ? 16u : 0u);
+    cp_async_16(dst + KdTile<D>::CODES + vr * (D / 2) + 16 * c, vc + off, in ? 16u : 0u);
+  }
+  if (lane < 16) {
+    const int c = lane & 7;                          // 4 steps a chunk (T_cap is a multiple of 16)
+    const bool in = j0 + 4 * c < T_cap;
+    const float* src = (lane < 8 ? ks : vs) + (in ? j0 + 4 * c : 0);
+    cp_async_16(dst + 2 * KdTile<D>::CODES + (lane < 8 ? 0 : KD_KT * 4) + 16 * c, src, in ? 16u : 0u);
+  }
+}
+
+template <int D, int NT, typename XT>
+__global__ void __launch_bounds__(32 * KD_WARPS)
+kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e) {
+  constexpr bool SPLIT = sizeof(XT) == 4;            // fp32: two fp16 terms for q and for the weights
+  constexpr int ROWS = 8 * NT;
+  constexpr int KW = D / 32, VW = D / 64;            // words of a key row, of a value row, a lane holds
+  constexpr int MT = D / 16;                         // 16-dimension tiles of the output
+  constexpr float BIAS = 10.f;
+  extern __shared__ __align__(16) uint8_t kd_smem[];
+  __shared__ float w_m[KD_WARPS][ROWS], w_l[KD_WARPS][ROWS];
+  __shared__ float c_m[ROWS], c_l[ROWS];
+  float* c_o = reinterpret_cast<float*>(kd_smem + KD_WARPS * KD_STAGES * KdTile<D>::BYTES);   // [ROWS][D]
+  pdl_launch_dependents();
+  pdl_wait();                                        // q and the cache come from the previous kernel
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  uint32_t csize, crank;
+  asm volatile("mov.u32 %0, %cluster_nctaid.x;" : "=r"(csize));
+  asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(crank));
+  const int group = a.heads / a.kv_heads;
+  const int b = blockIdx.z, h = blockIdx.y;
+  const int r0 = (int)(blockIdx.x / csize) * ROWS;   // first row (token * group + head of the group)
+  const int n_rows = kv_real_tokens(s, b) * group;
+  if (r0 >= n_rows) return;                          // the same for the whole cluster
+  const int nr = n_rows - r0 < ROWS ? n_rows - r0 : ROWS;
+  const int64_t p0 = kv_first_position(s, b);
+  const int64_t pf = p0 + r0 / group, pl = p0 + (r0 + nr - 1) / group;
+  const int p_lo = pf < 0 ? 0 : (pf < s.T_cap ? (int)pf : s.T_cap);
+  const int p_hi = pl < 0 ? -1 : (pl < s.T_cap ? (int)pl : s.T_cap - 1);
+  KeyTiles tiles = key_tiles<KD_KT>(p_lo, p_hi, a.window, a.sinks);
+  if (p_lo > p_hi) tiles.count = 0;                  // every query lies outside the cache
+
+  // ---- queries: row g of each 8 (scaled by a power of two), dimensions (D / 4) t .. ----
+  uint32_t qh[NT][2 * KW * 2], ql[SPLIT ? NT : 1][SPLIT ? 4 * KW : 1];
+  float unscale[NT][2];                              // of rows 2t, 2t + 1
+  int pos[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int rr = 8 * n + g;
+    const bool real = rr < nr;
+    const int R = r0 + rr;
+    const int l = R / group, hd = h * group + R - l * group;
+    const XT* src = static_cast<const XT*>(a.Q) + (((int64_t)b * s.L + l) * a.heads + hd) * D + (D / 4) * t;
+    float x[8 * KW];
+#pragma unroll
+    for (int i = 0; i < 8 * KW; ++i) x[i] = 0.f;
+    if (real) {
+      if constexpr (SPLIT) {
+#pragma unroll
+        for (int i = 0; i < 2 * KW; ++i) {
+          const uint4 u = ldg_v4(src + 4 * i);
+          x[4 * i] = __uint_as_float(u.x); x[4 * i + 1] = __uint_as_float(u.y);
+          x[4 * i + 2] = __uint_as_float(u.z); x[4 * i + 3] = __uint_as_float(u.w);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < KW; ++i) {
+          const uint4 u = ldg_v4(src + 8 * i);
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) { x[8 * i + 2 * j] = bf16lo(w[j]); x[8 * i + 2 * j + 1] = bf16hi(w[j]); }
+        }
+      }
+    }
+    float mx = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8 * KW; ++i) {
+      const float v = fabsf(x[i]);
+      mx = fmaxf(mx, v < INFINITY ? v : 0.f);
+    }
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    int e = (int)(__float_as_uint(mx) >> 23) - 127;
+    e = e < -100 ? -100 : e;
+    const float up = pow2i(14 - e);
+#pragma unroll
+    for (int i = 0; i < 4 * KW; ++i) {
+      const float lo = x[2 * i] * up, hi = x[2 * i + 1] * up;
+      qh[n][i] = pack_half2(lo, hi);
+      if constexpr (SPLIT) ql[n][i] = half2_rest(qh[n][i], lo, hi);
+    }
+    const float down = pow2i(e - 14) * scale_log2e;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      unscale[n][i] = __shfl_sync(0xffffffffu, down, 4 * (2 * t + i));
+      const int rc = 8 * n + 2 * t + i < nr ? 8 * n + 2 * t + i : nr - 1;
+      const int64_t p = p0 + (r0 + rc) / group;
+      pos[n][i] = p >= 0 && p < s.T_cap ? (int)p : -1;
+    }
+  }
+  const bool rows_in = pf >= 0 && pl < s.T_cap;
+
+  const int64_t head = (int64_t)b * a.kv_heads + h;
+  const uint8_t* kc = a.Kc + head * s.T_cap * (D / 2);
+  const uint8_t* vc = a.Vc + head * s.T_cap * (D / 2);
+  const float* ks = a.Ks + head * s.T_cap;
+  const float* vs = a.Vs + head * s.T_cap;
+  uint8_t* ring = kd_smem + warp * KD_STAGES * KdTile<D>::BYTES;
+
+  float m[NT][2], l[NT][2], o[NT][MT][4];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    m[n][0] = m[n][1] = -INFINITY;
+    l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) o[n][i][c] = 0.f;
+  }
+  const int first = (int)crank * KD_WARPS + warp, stride = (int)csize * KD_WARPS;
+  const int mine = tiles.count > first ? (tiles.count - first + stride - 1) / stride : 0;
+#pragma unroll
+  for (int i = 0; i < KD_STAGES - 1; ++i) {
+    if (i < mine)
+      kd_stage<D>(kc, ks, vc, vs, tiles.at(first + i * stride) * KD_KT, s.T_cap, ring + i * KdTile<D>::BYTES, lane);
+    cp_async_commit();
+  }
+  for (int it = 0; it < mine; ++it) {
+    asm volatile("cp.async.wait_group %0;" :: "n"(KD_STAGES - 2) : "memory");
+    __syncwarp();                                    // this tile is in place, and every lane is done with the last one
+    {
+      const int nx = it + KD_STAGES - 1;
+      if (nx < mine)
+        kd_stage<D>(kc, ks, vc, vs, tiles.at(first + nx * stride) * KD_KT, s.T_cap,
+                    ring + (nx % KD_STAGES) * KdTile<D>::BYTES, lane);
+      cp_async_commit();
+    }
+    const uint8_t* stage = ring + (it % KD_STAGES) * KdTile<D>::BYTES;
+    const float* kst = reinterpret_cast<const float*>(stage + 2 * KdTile<D>::CODES);
+    const float* vst = kst + KD_KT;
+    const int j0 = tiles.at(first + it * stride) * KD_KT;
+    // ---- scores of keys 16 x + g, + 8 (rows) and queries 2t, 2t + 1 (columns) ----
+    float sc[2][NT][4];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) sc[x][n][c] = 0.f;
+      const uint8_t* kr = stage + (16 * x + g) * (D / 2) + 4 * KW * t;
+      uint32_t w0[KW], w1[KW];
+      if constexpr (KW == 4) {
+        const uint4 u0 = *reinterpret_cast<const uint4*>(kr), u1 = *reinterpret_cast<const uint4*>(kr + 8 * (D / 2));
+        w0[0] = u0.x; w0[1] = u0.y; w0[2] = u0.z; w0[3] = u0.w;
+        w1[0] = u1.x; w1[1] = u1.y; w1[2] = u1.z; w1[3] = u1.w;
+      } else {
+        const uint2 u0 = *reinterpret_cast<const uint2*>(kr), u1 = *reinterpret_cast<const uint2*>(kr + 8 * (D / 2));
+        w0[0] = u0.x; w0[1] = u0.y;
+        w1[0] = u1.x; w1[1] = u1.y;
+      }
+#pragma unroll
+      for (int i = 0; i < KW; ++i) {
+        uint32_t k0[4], k1[4];
+        codes_to_half2(w0[i], k0);
+        codes_to_half2(w1[i], k1);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            mma_f16(sc[x][n], k0[2 * u], k1[2 * u], k0[2 * u + 1], k1[2 * u + 1], qh[n][4 * i + 2 * u],
+                    qh[n][4 * i + 2 * u + 1]);
+            if constexpr (SPLIT)
+              mma_f16(sc[x][n], k0[2 * u], k1[2 * u], k0[2 * u + 1], k1[2 * u + 1], ql[n][4 * i + 2 * u],
+                      ql[n][4 * i + 2 * u + 1]);
+          }
+        }
+      }
+    }
+    // ---- steps: scores in base-2 exponents, plus the value step's exponent ----
+    float f[2][2], inv[2][2];
+    const bool full = rows_in && j0 + KD_KT - 1 <= p_lo &&
+                      (a.window == 0 || j0 > p_hi - a.window || j0 + KD_KT <= a.sinks);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int key = 16 * x + 8 * y + g;
+        const float kstep = kst[key], vstep = vst[key];
+        const int e = step_exponent(vstep);
+        inv[x][y] = pow2i(-e);
+        f[x][y] = vstep * inv[x][y];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float v = sc[x][n][2 * y + i] * (kstep * unscale[n][i]) + (float)e;
+            sc[x][n][2 * y + i] = full || key_visible(j0 + key, pos[n][i], a.window, a.sinks) ? v : -INFINITY;
+          }
+      }
+    }
+    // ---- running maximum (a query's keys lie in the 8 lanes of one t), weights, sums ----
+    bool moved = false;
+    float corr[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float mx = fmaxf(fmaxf(sc[0][n][i], sc[0][n][2 + i]), fmaxf(sc[1][n][i], sc[1][n][2 + i]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+        const float mn = fmaxf(m[n][i], mx);
+        corr[n][i] = m[n][i] == mn ? 1.f : ex2(m[n][i] - mn);
+        moved |= m[n][i] != mn;
+        m[n][i] = mn;
+      }
+    if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          l[n][i] *= corr[n][i];
+#pragma unroll
+          for (int q = 0; q < MT; ++q) { o[n][q][i] *= corr[n][i]; o[n][q][2 + i] *= corr[n][i]; }
+        }
+    }
+    uint32_t ph[2][NT][2], pr[2][NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float ref0 = m[n][0] == -INFINITY ? 0.f : m[n][0] - BIAS;
+      const float ref1 = m[n][1] == -INFINITY ? 0.f : m[n][1] - BIAS;
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const float e0 = ex2(sc[x][n][2 * y] - ref0), e1 = ex2(sc[x][n][2 * y + 1] - ref1);
+          // a masked key's weight is zero whatever its steps hold
+          const bool s0 = sc[x][n][2 * y] != -INFINITY, s1 = sc[x][n][2 * y + 1] != -INFINITY;
+          l[n][0] += s0 ? e0 * inv[x][y] : 0.f;
+          l[n][1] += s1 ? e1 * inv[x][y] : 0.f;
+          const float w0 = s0 ? e0 * f[x][y] : 0.f, w1 = s1 ? e1 * f[x][y] : 0.f;
+          const uint32_t hi = pack_half2(w0, w1);
+          ph[x][n][y] = transpose8x8(hi);
+          if constexpr (SPLIT) pr[x][n][y] = transpose8x8(half2_rest(hi, w0, w1));
+        }
+    }
+    // ---- output: dimensions as the 16 rows, queries as the columns ----
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      uint32_t w[4][VW];                             // keys 2t, 2t + 1, 2t + 8, 2t + 9 of the 16
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint8_t* vr = stage + KdTile<D>::CODES + (16 * x + 8 * (k >> 1) + 4 * (k & 1) + t) * (D / 2) + 4 * VW * g;
+        if constexpr (VW == 2) {
+          const uint2 u = *reinterpret_cast<const uint2*>(vr);
+          w[k][0] = u.x; w[k][1] = u.y;
+        } else {
+          w[k][0] = *reinterpret_cast<const uint32_t*>(vr);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < VW; ++i) {
+        uint32_t a0[4], a1[4], a2[4], a3[4];         // even and odd dimensions of the key pairs
+        codes_to_half2(__byte_perm(w[0][i], w[1][i], 0x5410), a0);
+        codes_to_half2(__byte_perm(w[0][i], w[1][i], 0x7632), a1);
+        codes_to_half2(__byte_perm(w[2][i], w[3][i], 0x5410), a2);
+        codes_to_half2(__byte_perm(w[2][i], w[3][i], 0x7632), a3);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma_f16(o[n][4 * i + j], a0[j], a1[j], a2[j], a3[j], ph[x][n][0], ph[x][n][1]);
+            if constexpr (SPLIT) mma_f16(o[n][4 * i + j], a0[j], a1[j], a2[j], a3[j], pr[x][n][0], pr[x][n][1]);
+          }
+      }
+    }
+  }
+  cp_async_wait_all();
+  // ---- the warps' states into shared memory, merged over the warps ----
+  __syncthreads();                                   // every ring is free
+  float* w_o = reinterpret_cast<float*>(kd_smem);    // [KD_WARPS][ROWS][D]
+  static_assert(KD_WARPS * ROWS * D * 4 <= KD_WARPS * KD_STAGES * KdTile<D>::BYTES, "the partial outputs fit the rings");
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float sum = l[n][i];
+      sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+      const int row = 8 * n + 2 * t + i;
+      if (g == 0) { w_m[warp][row] = m[n][i]; w_l[warp][row] = sum; }
+      float* dst = w_o + ((size_t)warp * ROWS + row) * D + (D / 8) * g;     // dimensions (D / 8) g + 2 q, + 1
+#pragma unroll
+      for (int q = 0; q < MT; ++q) *reinterpret_cast<float2*>(dst + 2 * q) = make_float2(o[n][q][i], o[n][q][2 + i]);
+    }
+  __syncthreads();
+  if (tid < ROWS) {
+    float mx = w_m[0][tid];
+#pragma unroll
+    for (int w = 1; w < KD_WARPS; ++w) mx = fmaxf(mx, w_m[w][tid]);
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < KD_WARPS; ++w) {
+      const float c = w_m[w][tid] == -INFINITY ? 0.f : ex2(w_m[w][tid] - mx);
+      sum += w_l[w][tid] * c;
+      w_m[w][tid] = c;                               // the warp's factor
+    }
+    c_m[tid] = mx;
+    c_l[tid] = sum;
+  }
+  __syncthreads();
+  for (int e = tid; e < ROWS * D / 4; e += 32 * KD_WARPS) {
+    const int row = e / (D / 4);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < KD_WARPS; ++w) {
+      const float c = w_m[w][row];
+      const float4 v = *reinterpret_cast<const float4*>(w_o + (size_t)w * ROWS * D + 4 * e);
+      acc.x += c * v.x; acc.y += c * v.y; acc.z += c * v.z; acc.w += c * v.w;
+    }
+    *reinterpret_cast<float4*>(c_o + 4 * e) = acc;
+  }
+  // ---- merged over the cluster: each block takes a share of the outputs ----
+  cluster_arrive();
+  cluster_wait();
+  const uint32_t m_a = smem_u32(c_m), l_a = smem_u32(c_l), o_a = smem_u32(c_o);
+  for (int e = (int)crank * 32 * KD_WARPS + tid; e < nr * (D / 2); e += (int)csize * 32 * KD_WARPS) {
+    const int row = e / (D / 2), dim = 2 * (e - row * (D / 2));
+    float mx = -INFINITY;
+    for (uint32_t c = 0; c < csize; ++c) mx = fmaxf(mx, ld_cluster_f32(cluster_map(m_a + 4 * row, c)));
+    float sum = 0.f, x0 = 0.f, x1 = 0.f;
+    for (uint32_t c = 0; c < csize; ++c) {
+      const float mc = ld_cluster_f32(cluster_map(m_a + 4 * row, c));
+      const float w = mc == -INFINITY ? 0.f : ex2(mc - mx);
+      sum += w * ld_cluster_f32(cluster_map(l_a + 4 * row, c));
+      const uint32_t oa = cluster_map(o_a + 4 * (row * D + dim), c);
+      x0 += w * ld_cluster_f32(oa);
+      x1 += w * ld_cluster_f32(oa + 4);
+    }
+    const float r = mx == -INFINITY ? 0.f : 1.0f / sum;    // a query that sees no key: zeros
+    const int R = r0 + row, tok = R / group;
+    const int64_t off = (((int64_t)b * s.L + tok) * a.heads + h * group + R - tok * group) * D + dim;
+    if constexpr (SPLIT) {
+      *reinterpret_cast<float2*>(static_cast<float*>(a.A) + off) = make_float2(x0 * r, x1 * r);
+    } else {
+      *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(a.A) + off) = __floats2bfloat162_rn(x0 * r, x1 * r);
+    }
+  }
+  cluster_arrive();
+  cluster_wait();                                    // no block leaves while another reads its shared memory
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+template <int D, int NT, typename XT>
+static cudaError_t launch_decode(const KvStep& s, const AttnArgs& a, int64_t t_max, cudaStream_t st) {
+  constexpr int ROWS = 8 * NT;
+  auto kern = kv4_decode_kernel<D, NT, XT>;
+  const size_t smem = (size_t)KD_WARPS * KD_STAGES * KdTile<D>::BYTES + (size_t)ROWS * D * 4;
+  const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), smem);
+  if (e != cudaSuccess) return e;
+  const int64_t row_tiles = ((int64_t)s.L * (a.heads / a.kv_heads) + ROWS - 1) / ROWS;
+  // a cluster splits the keys of one row tile: as long as the blocks fit the GPU two
+  // or three to an SM and every warp has a few tiles
+  const int64_t blocks = row_tiles * a.kv_heads * s.B;
+  int64_t keys = t_max;
+  if (a.window > 0 && (int64_t)a.window + a.sinks + s.L < keys) keys = (int64_t)a.window + a.sinks + s.L;
+  unsigned c = 1;
+  while (c < 8 && blocks * c * 2 <= 3 * 148 && keys > (int64_t)c * KD_WARPS * KD_KT * 2) c *= 2;
+  return launch_pdl(kern, dim3((unsigned)(row_tiles * c), (unsigned)a.kv_heads, (unsigned)s.B), dim3(32 * KD_WARPS),
+                    smem, st, dim3(c, 1, 1), s, a, (float)(1.4426950408889634 / sqrt((double)D)));
+}
+
+template <int D, typename XT>
+static cudaError_t launch_attention(const KvStep& s, const AttnArgs& a, int64_t t_max, cudaStream_t st) {
+  if ((int64_t)s.L * (a.heads / a.kv_heads) <= 8) return launch_decode<D, 1, XT>(s, a, t_max, st);
+  return launch_decode<D, 2, XT>(s, a, t_max, st);
+}
+
+cudaError_t run_kv4_attention(const KvStep& s, const AttnArgs& a, int bf16, int d, int64_t t_max, cudaStream_t st) {
+  using bf = __nv_bfloat16;
+  if (d == 128) return bf16 ? launch_attention<128, bf>(s, a, t_max, st) : launch_attention<128, float>(s, a, t_max, st);
+  return bf16 ? launch_attention<64, bf>(s, a, t_max, st) : launch_attention<64, float>(s, a, t_max, st);
+}
+
+}  // namespace bitnet

@@ -1,0 +1,82 @@
+// What the kernels around the 4-bit key/value cache share (sm_100a only).
+//
+// Cache layout: codes [B][kv_heads][T_cap][d/2] bytes and steps [B][kv_heads][T_cap]
+// fp32, for keys and for values: the rows of one sequence's head are contiguous,
+// so a block of keys is one run of bytes.  A row stands for code * step.  Of the 8
+// codes of a little-endian 32-bit word, code 2j + i (i = 0, 1) sits at bits
+// 4j + 16i, two's complement: (word >> 4j) & 0x000F000F is the pair of codes
+// (2j, 2j + 1) in the two halves of a register, in order.
+#pragma once
+
+#include "common.cuh"
+
+namespace bitnet {
+
+// Where the tokens of a step sit: token l of sequence b is row b * L + l of the
+// step's tensors and position t0 + pos[b] + l of its sequence; the first len[b]
+// tokens of a sequence are real, the others padding.
+struct KvStep {
+  const int32_t* pos;                               // [B] or NULL (zeros)
+  const int32_t* len;                               // [B] or NULL (L)
+  int64_t t0;
+  int B, L, T_cap;
+};
+
+BN_DEV int kv_real_tokens(const KvStep& s, int b) {
+  if (s.len == nullptr) return s.L;
+  const int n = s.len[b];
+  return n < 0 ? 0 : (n < s.L ? n : s.L);
+}
+BN_DEV int64_t kv_first_position(const KvStep& s, int b) {
+  return s.t0 + (s.pos == nullptr ? 0 : (int64_t)s.pos[b]);
+}
+
+// The append's rows, factors and destinations (fp32 caches or 4-bit ones).
+struct RopeTable { double theta[64]; };             // theta_i of the pairs that turn
+
+struct AppendArgs {
+  const void *Q, *K, *V;
+  int64_t ldq, ldk, ldv;                            // row strides, in values
+  const float *gamma_q, *gamma_k;
+  float eps;
+  int heads, kv_heads, rot_dim, norm, hadamard;
+  void* Qo;
+  int qo_bf16;
+  float *Kc32, *Vc32;                               // fp32 caches [B][T_cap][kv_heads * d]
+  uint8_t *Kc4, *Vc4;                               // 4-bit caches
+  float *Ks, *Vs;
+};
+
+// The attention's operands.
+struct AttnArgs {
+  const void* Q;                                    // [B * L][heads * d]
+  const uint8_t *Kc, *Vc;
+  const float *Ks, *Vs;
+  void* A;                                          // [B * L][heads * d]
+  int heads, kv_heads;
+  int window, sinks;                                // window 0: every key up to the query's own
+};
+
+// Four code pairs of a word as fp16 pairs, exact: a code's nibble with its sign
+// bit flipped is code + 8, which as the low mantissa bits of 1024 (nibbles 0 and
+// 2 of each half) or the next four (1 and 3) needs one subtraction, or one
+// multiply-add, to become the code.
+BN_DEV uint32_t h2_sub(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+BN_DEV uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+BN_DEV void codes_to_half2(uint32_t w, uint32_t (&p)[4]) {
+  const uint32_t v = w >> 8;
+  p[0] = h2_sub((w & 0x000F000Fu) ^ 0x64086408u, 0x64086408u);                 // 1024 + u - 1032
+  p[1] = h2_fma((w & 0x00F000F0u) ^ 0x64806480u, 0x2C002C00u, 0xD480D480u);    // (1024 + 16 u) / 16 - 72
+  p[2] = h2_sub((v & 0x000F000Fu) ^ 0x64086408u, 0x64086408u);
+  p[3] = h2_fma((v & 0x00F000F0u) ^ 0x64806480u, 0x2C002C00u, 0xD480D480u);
+}
+
+}  // namespace bitnet

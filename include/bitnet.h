@@ -326,6 +326,100 @@ BITNET_API int bitnet_attention(const float* Q, const float* Kc, const float* Vc
                                 int heads, int head_dim, int64_t T_cap, float* A, void* stream);
 
 /*
+ * The attention core with norms of queries and keys, shared key heads, ragged
+ * steps and a key/value cache held in 4 bits.  The pages name neither; [P1
+ * 방법론] gives the Hadamard transform ahead of a 4-bit quantiser, which is used
+ * here for the keys, with the absmax rule of bitnet_hadamard_quant_act.
+ *
+ * A step: B sequences bring L token rows each.  Token l of sequence b is row
+ * b*L + l of Q, K, V, Qo and A, at position t0 + pos[b] + l of its sequence.
+ *   pos : [B] int32 on the device, or NULL (zeros); read when the kernels run,
+ *         so that a captured step can be replayed at other positions.
+ *   len : [B] int32 on the device, or NULL: only the first len[b] tokens of
+ *         sequence b are real (clamped to 0 .. L); the rows behind them are
+ *         padding, never read and left as they were in every output.
+ *   A position outside 0 .. T_cap-1 is not appended (its Qo row is written) and
+ *   not read back; its attention row is zero.  With pos == NULL the host refuses
+ *   t0 + L > T_cap instead.
+ * Heads: `heads` query heads share `kv_heads` key heads (heads % kv_heads == 0);
+ *   query head q reads key head q / (heads / kv_heads).  head_dim 64 or 128.
+ * Rows of Q, K, V are contiguous, ldq / ldk / ldv values apart (views of one
+ *   fused projection are fine); a stride in bytes is a multiple of 16.
+ * Per row x of d = head_dim values at position p:
+ *   norm      y = x / sqrt(mean(x^2) + eps) * gamma       (queries and keys)
+ *   rotation  the pairs (y[2i], y[2i+1]), i < rot_dim / 2, turn by the angle
+ *             p * base^(-2i / rot_dim)                    (queries and keys)
+ *   Hadamard  y H / sqrt(d), Sylvester order as in bitnet_hadamard_quant_act
+ *             (queries and keys, so that every product q . k stays as it is)
+ *   4 bits    t = fp32(y);  s = 7 / max(max|t|, 1e-5);  code = clamp(rint(t * s),
+ *             -8, 7);  step = 1 / s.  The row stands for code * step.
+ *   Keys of the 4-bit cache are computed in fp64 up to t, queries and fp32 caches
+ *   in fp32 (angles in fp64).  Values are finite.
+ * 4-bit caches: codes Kc, Vc [B][kv_heads][T_cap][d/2] bytes, steps Ks, Vs
+ *   [B][kv_heads][T_cap] fp32, T_cap % 16 == 0.  Of each 8 codes of a row (one
+ *   little-endian 32-bit word), code 2j + i (i = 0, 1) sits at bits 4j + 16i, two's
+ *   complement.
+ * Limits of all four: B, L >= 0 (0 is a no-op), B <= 65535, B*L*heads < 2^31,
+ *   1 <= heads <= 256, 0 <= t0, 1 <= T_cap <= 2^24, B*T_cap*kv_heads*d < 2^40.
+ *
+ * bitnet_qk_norm_rope_append: bitnet_rope_append with norms.  Qo [B*L][heads*d]
+ *   fp32 receives the turned queries (it may be Q itself where x_dtype is
+ *   BITNET_F32 and ldq == heads*d); Kc, Vc [B][T_cap][kv_heads*d] fp32 the turned
+ *   keys and the values.  gamma_q, gamma_k: [d] fp32 or NULL (ones).  rot_dim: even,
+ *   0 .. d.  base > 1.
+ */
+BITNET_API int bitnet_qk_norm_rope_append(const void* Q, const void* K, const void* V, int x_dtype, int64_t ldq,
+                                          int64_t ldk, int64_t ldv, int64_t B, int64_t L, int64_t t0,
+                                          const int32_t* pos, const int32_t* len, int heads, int kv_heads,
+                                          int head_dim, const float* gamma_q, const float* gamma_k, float eps,
+                                          int rot_dim, double base, float* Qo, float* Kc, float* Vc, int64_t T_cap,
+                                          void* stream);
+
+/*
+ * bitnet_kv4_append: the same pass into a 4-bit cache.  flags: BITNET_KV_NORM
+ *   (without it gamma_q and gamma_k are not read) and BITNET_KV_HADAMARD.  Qo
+ *   [B*L][heads*d] in q_dtype (it may be Q itself where q_dtype is x_dtype and
+ *   ldq == heads*d).
+ */
+enum { BITNET_KV_NORM = 1, BITNET_KV_HADAMARD = 2 };
+BITNET_API int bitnet_kv4_append(const void* Q, const void* K, const void* V, int x_dtype, int64_t ldq, int64_t ldk,
+                                 int64_t ldv, int64_t B, int64_t L, int64_t t0, const int32_t* pos,
+                                 const int32_t* len, int heads, int kv_heads, int head_dim, const float* gamma_q,
+                                 const float* gamma_k, float eps, int rot_dim, double base, int flags, void* Qo,
+                                 int q_dtype, uint8_t* Kc, float* Ks, uint8_t* Vc, float* Vs, int64_t T_cap,
+                                 void* stream);
+
+/*
+ * bitnet_kv4_read: the values that the cache holds for the tokens of a step (for
+ *   instance a prefix that is handed on): K, V [B*L][kv_heads*d] in dtype, code *
+ *   step rounded once to fp32 (then to bf16).  K or V may be NULL (not wanted), with
+ *   its codes and steps.  Keys come as they are held, turned (and transformed where
+ *   they were appended with BITNET_KV_HADAMARD).
+ */
+BITNET_API int bitnet_kv4_read(const uint8_t* Kc, const float* Ks, const uint8_t* Vc, const float* Vs, int64_t B,
+                               int64_t L, int64_t t0, const int32_t* pos, const int32_t* len, int kv_heads,
+                               int head_dim, int64_t T_cap, void* K, void* V, int dtype, void* stream);
+
+/*
+ * bitnet_kv4_attention: A row = softmax(q . k / sqrt(d)) v over the keys j of its
+ *   sequence with j <= p, and, where window > 0, with j > p - window or j < sinks
+ *   (a sliding window behind a few first tokens that stay visible).  The cache must
+ *   hold the keys up to the step's own already, with steps as bitnet_kv4_append
+ *   writes them (0, or 1e-5 / 7 and more; below 2^60).
+ * Q, A   : [B*L][heads*d] in dtype (A may be Q itself).
+ * window : 0 (every key) or the number of keys of the window; sinks >= 0.
+ * t_max  : a bound on the positions in use plus one, 1 .. T_cap, or 0 (T_cap).  It
+ *          only steers how the work is split over the GPU.
+ * fp32 softmax; products with fp16 operands that hold the codes exactly, bf16
+ * queries to 11 bits and more and fp32 queries to 22 bits, and the weights to 11
+ * (bf16) or 22 bits (fp32).
+ */
+BITNET_API int bitnet_kv4_attention(const void* Q, int dtype, const uint8_t* Kc, const float* Ks, const uint8_t* Vc,
+                                    const float* Vs, int64_t B, int64_t L, int64_t t0, const int32_t* pos,
+                                    const int32_t* len, int heads, int kv_heads, int head_dim, int64_t T_cap,
+                                    int64_t window, int64_t sinks, int64_t t_max, void* A, void* stream);
+
+/*
  * Reads and clears the library's device-side error flag on the current
  * device (synchronises the device).  A kernel that waited more than ~2 s on
  * a pipeline barrier gives up, records a nonzero code here and returns; 0
