@@ -47,6 +47,7 @@ cudaError_t run_attention(const float* Q, const float* Kc, const float* Vc, int 
 cudaError_t run_append(const KvStep& s, const AppendArgs& a, int x_bf16, int d, double base, cudaStream_t st);
 cudaError_t run_kv4_read(const KvStep& s, int kv_heads, int d, const uint8_t* Kc, const float* Ks, const uint8_t* Vc,
                          const float* Vs, void* K, void* V, int bf16, cudaStream_t st);
+cudaError_t kv4_prefill_error(int* code);
 cudaError_t run_kv4_attention(const KvStep& s, const AttnArgs& a, int bf16, int d, int64_t t_max, cudaStream_t st);
 }  // namespace bitnet
 
@@ -558,14 +559,15 @@ int bitnet_kv4_attention(const void* Q, int dtype, const uint8_t* Kc, const floa
 }
 
 int bitnet_device_error(int* code_out) {
-  int code = 0, zero = 0;
+  int code = 0, other = 0, zero = 0;
   if (cudaDeviceSynchronize() != cudaSuccess) { cudaGetLastError(); return BITNET_ERR_CUDA; }
   if (cudaMemcpyFromSymbol(&code, bitnet::g_device_error, sizeof(int)) != cudaSuccess ||
-      cudaMemcpyToSymbol(bitnet::g_device_error, &zero, sizeof(int)) != cudaSuccess) {
+      cudaMemcpyToSymbol(bitnet::g_device_error, &zero, sizeof(int)) != cudaSuccess ||
+      bitnet::kv4_prefill_error(&other) != cudaSuccess) {
     cudaGetLastError();
     return BITNET_ERR_CUDA;
   }
-  if (code_out) *code_out = code;
+  if (code_out) *code_out = code != 0 ? code : other;
   return BITNET_OK;
 }
 

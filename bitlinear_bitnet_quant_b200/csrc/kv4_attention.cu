@@ -19,25 +19,8 @@
 #include "kv4_common.cuh"
 
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 
 namespace bitnet {
-
-BN_DEV float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-BN_DEV uint32_t pack_half2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-// What the fp16 pair h leaves of (lo, hi), as another fp16 pair.
-BN_DEV uint32_t half2_rest(uint32_t h, float lo, float hi) {
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  return pack_half2(lo - f.x, hi - f.y);
-}
 
 // A step's exponent e, at least -24: the append writes steps of 2^-20 and more (or a
 // row is empty, step 0, and keeps its weight in the sum).  Together with steps below
@@ -48,31 +31,6 @@ BN_DEV int step_exponent(float step) {
   return e < -24 ? -24 : (e > 126 ? 126 : e);
 }
 BN_DEV float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
-
-// The key tiles (of KT keys) that some query of positions p_lo .. p_hi sees: those
-// of the sinks, then those from the first query's window on.
-struct KeyTiles {
-  int sink_tiles, first, count;
-  BN_DEV int at(int i) const { return i < sink_tiles ? i : first + i - sink_tiles; }
-};
-template <int KT>
-BN_DEV KeyTiles key_tiles(int p_lo, int p_hi, int window, int sinks) {
-  KeyTiles k;
-  const int hi = p_hi + 1;
-  int lo = 0, sk = 0;
-  if (window > 0) {
-    lo = p_lo - window + 1 > 0 ? p_lo - window + 1 : 0;
-    sk = sinks < hi ? sinks : hi;
-  }
-  k.sink_tiles = (sk + KT - 1) / KT;
-  k.first = lo / KT > k.sink_tiles ? lo / KT : k.sink_tiles;
-  const int end = (hi + KT - 1) / KT;
-  k.count = k.sink_tiles + (end > k.first ? end - k.first : 0);
-  return k;
-}
-BN_DEV bool key_visible(int j, int p, int window, int sinks) {
-  return j <= p && (window == 0 || j > p - window || j < sinks);
-}
 
 // ---------------------------------------------------------------------------
 // few queries a key head: warp-level products (m16n8k16), keys as the 16 rows and
@@ -478,6 +436,8 @@ kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e) {
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
+cudaError_t run_kv4_prefill(const KvStep& s, const AttnArgs& a, int d, cudaStream_t st);
+
 template <int D, int NT, typename XT>
 static cudaError_t launch_decode(const KvStep& s, const AttnArgs& a, int64_t t_max, cudaStream_t st) {
   constexpr int ROWS = 8 * NT;
@@ -499,6 +459,9 @@ static cudaError_t launch_decode(const KvStep& s, const AttnArgs& a, int64_t t_m
 
 template <int D, typename XT>
 static cudaError_t launch_attention(const KvStep& s, const AttnArgs& a, int64_t t_max, cudaStream_t st) {
+  if constexpr (sizeof(XT) == 2) {
+    if ((int64_t)s.L * (a.heads / a.kv_heads) >= 128) return run_kv4_prefill(s, a, D, st);
+  }
   if ((int64_t)s.L * (a.heads / a.kv_heads) <= 8) return launch_decode<D, 1, XT>(s, a, t_max, st);
   return launch_decode<D, 2, XT>(s, a, t_max, st);
 }

@@ -8,6 +8,8 @@
 // (2j, 2j + 1) in the two halves of a register, in order.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 
 namespace bitnet {
@@ -77,6 +79,47 @@ BN_DEV void codes_to_half2(uint32_t w, uint32_t (&p)[4]) {
   p[1] = h2_fma((w & 0x00F000F0u) ^ 0x64806480u, 0x2C002C00u, 0xD480D480u);    // (1024 + 16 u) / 16 - 72
   p[2] = h2_sub((v & 0x000F000Fu) ^ 0x64086408u, 0x64086408u);
   p[3] = h2_fma((v & 0x00F000F0u) ^ 0x64806480u, 0x2C002C00u, 0xD480D480u);
+}
+
+BN_DEV float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+BN_DEV uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// What the fp16 pair h leaves of (lo, hi), as another fp16 pair.
+BN_DEV uint32_t half2_rest(uint32_t h, float lo, float hi) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return pack_half2(lo - f.x, hi - f.y);
+}
+
+// The key tiles (of KT keys) that some query of positions p_lo .. p_hi sees: those
+// of the sinks, then those from the first query's window on.
+struct KeyTiles {
+  int sink_tiles, first, count;
+  BN_DEV int at(int i) const { return i < sink_tiles ? i : first + i - sink_tiles; }
+};
+template <int KT>
+BN_DEV KeyTiles key_tiles(int p_lo, int p_hi, int window, int sinks) {
+  KeyTiles k;
+  const int hi = p_hi + 1;
+  int lo = 0, sk = 0;
+  if (window > 0) {
+    lo = p_lo - window + 1 > 0 ? p_lo - window + 1 : 0;
+    sk = sinks < hi ? sinks : hi;
+  }
+  k.sink_tiles = (sk + KT - 1) / KT;
+  k.first = lo / KT > k.sink_tiles ? lo / KT : k.sink_tiles;
+  const int end = (hi + KT - 1) / KT;
+  k.count = k.sink_tiles + (end > k.first ? end - k.first : 0);
+  return k;
+}
+BN_DEV bool key_visible(int j, int p, int window, int sinks) {
+  return j <= p && (window == 0 || j > p - window || j < sinks);
 }
 
 }  // namespace bitnet
