@@ -22,16 +22,6 @@
 
 namespace bitnet {
 
-// A step's exponent e, at least -24: the append writes steps of 2^-20 and more (or a
-// row is empty, step 0, and keeps its weight in the sum).  Together with steps below
-// 2^60 no weight p' that counts leaves the range of fp32 (2^-126): 2^(-24 - 60) of
-// the largest one, times the weight itself.
-BN_DEV int step_exponent(float step) {
-  const int e = (int)((__float_as_uint(step) >> 23) & 255u) - 127;
-  return e < -24 ? -24 : (e > 126 ? 126 : e);
-}
-BN_DEV float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
-
 // ---------------------------------------------------------------------------
 // few queries a key head: warp-level products (m16n8k16), keys as the 16 rows and
 // queries as the 8 columns, so that up to 8 queries (the heads that share a key
@@ -162,8 +152,7 @@ kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e) {
     }
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    int e = (int)(__float_as_uint(mx) >> 23) - 127;
-    e = e < -100 ? -100 : e;
+    const int e = row_exponent(mx);
     const float up = pow2i(14 - e);
 #pragma unroll
     for (int i = 0; i < 4 * KW; ++i) {

@@ -97,6 +97,21 @@ BN_DEV uint32_t half2_rest(uint32_t h, float lo, float hi) {
   return pack_half2(lo - f.x, hi - f.y);
 }
 
+// A step's exponent e, at least -24: the append writes steps of 2^-20 and more (or a
+// row is empty, step 0, and keeps its weight in the sum).  Together with steps below
+// 2^60 no weight p' that counts leaves the range of fp32 (2^-126): 2^(-24 - 60) of
+// the largest one, times the weight itself.
+BN_DEV int step_exponent(float step) {
+  const int e = (int)((__float_as_uint(step) >> 23) & 255u) - 127;
+  return e < -24 ? -24 : (e > 126 ? 126 : e);
+}
+BN_DEV float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+// The exponent of a row's largest finite value, so that 2^e and 2^-e are normal numbers.
+BN_DEV int row_exponent(float v) {
+  const int e = (int)(__float_as_uint(v) >> 23) - 127;
+  return e < -100 ? -100 : e;
+}
+
 // The key tiles (of KT keys) that some query of positions p_lo .. p_hi sees: those
 // of the sinks, then those from the first query's window on.
 struct KeyTiles {

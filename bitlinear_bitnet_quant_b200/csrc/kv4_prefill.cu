@@ -1,8 +1,7 @@
 // Causal attention over the 4-bit key/value cache for many queries a key head
-// (prefill), on tcgen05.  The method is that of the few-query kernel beside it
-// (scores and weights as there, with the value step's logarithm in the weight's
-// exponent); this file is compiled as a whole program, so that its warps can share
-// the register file unevenly, and keeps its own copy of the error flag.
+// (prefill), on tcgen05.  This file is compiled as a whole program, so that its
+// warps can share the register file unevenly, and keeps its own copy of the error
+// flag.
 #define BITNET_OWN_ERROR_FLAG
 #include "kv4_common.cuh"
 
@@ -11,27 +10,45 @@
 namespace bitnet {
 
 // ---------------------------------------------------------------------------
-// many queries a key head (prefill): tcgen05.  A block takes 256 rows (token,
-// head of the group) of one key head as two streams of 128, which share every tile
-// of 128 keys: four warps unpack a tile's codes from global memory into 128-byte
-// swizzled fp16 operands in shared memory (two stages), one thread issues the
-// products, and four warps a stream turn scores into weights, one row a thread.
-//   scores  Q (shared memory, bf16) x codes (bf16) -> tensor memory, fp32
+// A block takes 256 rows (token, head of the group) of one key head as two streams
+// of 128, which share every tile of 128 keys: four warps unpack a tile from global
+// memory into 128-byte swizzled fp16 operands in shared memory (two stages), one
+// warp issues the products, and four warps a stream turn scores into weights, one
+// row a thread.
+//   scores  q (shared memory) x keys -> tensor memory, fp32
 //   weights written over the scores as fp16, the product's operand in tensor memory
-//   output  weights x codes (fp16, keys as the reduction) -> tensor memory, fp32
+//   output  weights x values (keys as the reduction) -> tensor memory, fp32
 // While one stream's weights are computed, the other stream's products run.
-// The running maximum is moved only when a row exceeds it by 2^8 (the weights then
-// stay below 2^15): the output in tensor memory is rescaled rarely.
+//
+// Operands.  A query row is scaled by a power of two (bf16 values are then exact in
+// fp16).  A tile's keys are code * step * 2^(11 - E) in fp16, E the exponent of the
+// tile's largest step, rounded once (2^-11 of a value, as the weights are); values the
+// same with E = F.  A row's score in base-2 exponents is then acc * c with one factor
+// c a row and tile, and its weight carries the tile's 2^F, p' = 2^(acc c + F - m): the
+// output sums p' v 2^(11 - F) over all tiles in one scale, and the softmax sum takes
+// 2^-F once a tile.  The running maximum m is that of acc c + F; it is moved only when
+// a row exceeds it by 2^8 (the weights then stay below 2^15), so the output in tensor
+// memory is rescaled rarely.  Steps in the softmax instead (a factor, an exponent and
+// a reciprocal a key, read from shared memory) took 3000 cycles a stream and tile.
 // ---------------------------------------------------------------------------
 constexpr int KP_KT = 128;                           // keys a tile
+constexpr int KP_STEPS = 4;                          // tiles whose steps are held: a stream may be two tiles behind
 constexpr int KP_THREADS = 512;                      // streams: warps 0-3 and 4-7; unpackers 8-11; products: warp 12
 
 template <int D>
 struct KpSmem {
   static constexpr int TILE = 128 * D * 2;           // 128 rows of D 16-bit values
-  static constexpr int Q = 0, K = 2 * TILE, V = 4 * TILE, STEPS = 6 * TILE;   // 2 of each
-  static constexpr int BYTES = STEPS + 2 * 3 * KP_KT * 4 + 1024;              // + alignment of the base
+  static constexpr int Q = 0, K = 2 * TILE, V = 4 * TILE, BYTES = 6 * TILE + 1024;   // 2 of each, + alignment
 };
+
+// One lane of a warp that runs as a whole.  The compiler knows the lane to be alone
+// (unlike a test of the lane's number), so the products' descriptors stay in uniform
+// registers: issued from a lane-number branch, a product took 300 cycles instead of 64.
+BN_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
 
 BN_DEV uint64_t pack_f2(float lo, float hi) {
   uint64_t r;
@@ -95,16 +112,12 @@ BN_DEV void tmem_ld32(uint32_t taddr, uint32_t* v) {
       : "r"(taddr) : "memory");
 }
 
-// Four code pairs of a word as bf16 pairs, exact (the nibble as the low mantissa bits of 128).
-BN_DEV uint32_t bf2_sub(uint32_t a, uint32_t b) {
+BN_DEV uint32_t h2_mul(uint32_t a, uint32_t b) {
   uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-BN_DEV void codes_to_bf2(uint32_t w, uint32_t (&p)[4]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) p[j] = bf2_sub(((w >> (4 * j)) & 0x000F000Fu) ^ 0x43084308u, 0x43084308u);
-}
+BN_DEV uint32_t both_halves(float v) { return pack_half2(v, v); }
 
 // Positions of one stream's rows, and what of a key tile they see.
 struct KpRows {
@@ -137,9 +150,10 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, float scale_log2e, int row_
   extern __shared__ uint8_t kp_raw[];
   __shared__ uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2], q_full, s_full[2], p_full[2], o_full[2];
   __shared__ uint32_t tmem_sh;
+  __shared__ __align__(16) uint32_t step_top[2][2][4];        // read as 16 bytes
+  __shared__ float2 steps[KP_STEPS];                  // of a tile: the scores' factor, F
   uint8_t* sm = smem_align(kp_raw, 1024);
-  float* steps = reinterpret_cast<float*>(sm + M::STEPS);      // [stage][3][KP_KT]
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], 128);
@@ -175,9 +189,8 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, float scale_log2e, int row_
   const int64_t p0 = kv_first_position(s, b);
   const KpRows rows0 = kp_rows(r0, n_rows, group, p0, s.T_cap), rows1 = kp_rows(r0 + 128, n_rows, group, p0, s.T_cap);
   KeyTiles tiles = {0, 0, 0};
-  if (rows0.n > 0 || rows1.n > 0)
-    tiles = key_tiles<KP_KT>(rows0.n > 0 ? rows0.p_lo : rows1.p_lo, rows1.n > 0 ? rows1.p_hi : rows0.p_hi, a.window,
-                             a.sinks);
+  const int first_seen = rows0.n > 0 ? rows0.p_lo : rows1.p_lo, last_seen = rows1.n > 0 ? rows1.p_hi : rows0.p_hi;
+  if (rows0.n > 0 || rows1.n > 0) tiles = key_tiles<KP_KT>(first_seen, last_seen, a.window, a.sinks);
   const int64_t head = (int64_t)b * a.kv_heads + h;
 
   if (r0 < n_rows) {
@@ -192,15 +205,38 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, float scale_log2e, int row_
       const int64_t off = (((int64_t)b * s.L + tok) * a.heads + h * group + R - tok * group) * D;
       const int64_t pr = p0 + tok;
       const int p = real && pr >= 0 && pr < s.T_cap ? (int)pr : -1;
+      float row_scale;                               // base-2 score of an accumulator, up to the tile's factor
       {
-        // the row's bf16 values, K-major with 128-byte swizzle
+        // the row's values, scaled, K-major with 128-byte swizzle
         uint8_t* dst = sm + M::Q + g * M::TILE + row * 128;
         const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.Q) + off;
+        uint4 v[D / 8];
+        float mx = 0.f;
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (real) v = ldg_v4(src + 8 * c);
-          *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + (((c & 7) ^ (row & 7)) << 4)) = v;
+          v[c] = make_uint4(0u, 0u, 0u, 0u);
+          if (real) v[c] = ldg_v4(src + 8 * c);
+        }
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float lo = fabsf(bf16lo(w[j])), hi = fabsf(bf16hi(w[j]));
+            mx = max3(mx, lo < INFINITY ? lo : 0.f, hi < INFINITY ? hi : 0.f);
+          }
+        }
+        const int e = row_exponent(mx);
+        const float up = pow2i(14 - e);
+        row_scale = pow2i(e - 14);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+          uint32_t o[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[j] = pack_half2(bf16lo(w[j]) * up, bf16hi(w[j]) * up);
+          *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + (((c & 7) ^ (row & 7)) << 4)) =
+              make_uint4(o[0], o[1], o[2], o[3]);
         }
         fence_proxy_async_smem();
         mbar_arrive(&q_full);
@@ -208,7 +244,7 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, float scale_log2e, int row_
       const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
       const uint32_t S = lanes + S_COL + 128u * g, O = lanes + O_COL + 128u * g;
       float m = -INFINITY;
-      uint64_t l2 = 0;
+      float l = 0.f;
       bool started = false, ok = true;
       int seen = 0;
       for (int i = 0; i < tiles.count && ok; ++i) {
@@ -219,20 +255,14 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, float scale_log2e, int row_
         ++seen;
         if (!ok) break;
         tc_fence_after();
-        const float* ks = steps + (i & 1) * 3 * KP_KT;
+        const float2 st = steps[i % KP_STEPS];
+        const float f = st.x * row_scale, F = st.y;
         float x[KP_KT];
         {
           uint32_t* xr = reinterpret_cast<uint32_t*>(x);
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld32(S + 32 * c, xr + 32 * c);
           tmem_wait_ld();
-        }
-#pragma unroll
-        for (int c = 0; c < KP_KT; c += 4) {
-          const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(ks + c);
-          const ulonglong2 e = *reinterpret_cast<const ulonglong2*>(ks + KP_KT + c);
-          unpack_f2(fma_f2(pack_f2(x[c], x[c + 1]), k.x, e.x), x[c], x[c + 1]);
-          unpack_f2(fma_f2(pack_f2(x[c + 2], x[c + 3]), k.y, e.y), x[c + 2], x[c + 3]);
         }
         if (!rows.full(j0, a.window, a.sinks)) {
           const int hi = p - j0;                                       // columns up to hi, and past lo or below sk
@@ -246,13 +276,12 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, float scale_log2e, int row_
           mx = max3(mx, x[c], x[c + 1]);
           my = max3(my, x[c + 2], x[c + 3]);
         }
-        mx = max3(mx, my, fmaxf(x[KP_KT - 2], x[KP_KT - 1]));
+        mx = max3(mx, my, fmaxf(x[KP_KT - 2], x[KP_KT - 1])) * f + F;
         if (__any_sync(0xffffffffu, mx > m + MOVE || (m == -INFINITY && mx != -INFINITY))) {
           const float mn = fmaxf(m, mx);
-          const float f = m == -INFINITY ? 0.f : ex2(m - mn);
-          const uint64_t f2 = pack_f2(f, f);
+          const float down = m == -INFINITY ? 0.f : ex2(m - mn);
           m = mn;
-          l2 = fma_f2(l2, f2, 0ull);
+          l *= down;
           if (started) {                                               // this stream's products so far are complete
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
@@ -260,26 +289,31 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, float scale_log2e, int row_
               tmem_ld32(O + c, v);
               tmem_wait_ld();
 #pragma unroll
-              for (int q = 0; q < 32; ++q) v[q] = __float_as_uint(__uint_as_float(v[q]) * f);
+              for (int q = 0; q < 32; ++q) v[q] = __float_as_uint(__uint_as_float(v[q]) * down);
               tmem_st32(O + c, v);
             }
           }
         }
         started = true;
-        const float ref = m == -INFINITY ? 0.f : BIAS - m;
-        const uint64_t ref2 = pack_f2(ref, ref);
+        const float ref = m == -INFINITY ? 0.f : BIAS + F - m;
+        const uint64_t ref2 = pack_f2(ref, ref), f2 = pack_f2(f, f);
+        uint64_t l2 = 0, l3 = 0;
         uint32_t w[KP_KT / 2];
 #pragma unroll
         for (int c = 0; c < KP_KT; c += 4) {
-          const ulonglong2 iv = *reinterpret_cast<const ulonglong2*>(ks + 2 * KP_KT + c);
           float e0, e1, e2, e3;
-          unpack_f2(add_f2(pack_f2(x[c], x[c + 1]), ref2), e0, e1);
-          unpack_f2(add_f2(pack_f2(x[c + 2], x[c + 3]), ref2), e2, e3);
+          unpack_f2(fma_f2(pack_f2(x[c], x[c + 1]), f2, ref2), e0, e1);
+          unpack_f2(fma_f2(pack_f2(x[c + 2], x[c + 3]), f2, ref2), e2, e3);
           e0 = ex2(e0); e1 = ex2(e1); e2 = ex2(e2); e3 = ex2(e3);
-          l2 = fma_f2(pack_f2(e0, e1), iv.x, l2);
-          l2 = fma_f2(pack_f2(e2, e3), iv.y, l2);
+          l2 = add_f2(l2, pack_f2(e0, e1));
+          l3 = add_f2(l3, pack_f2(e2, e3));
           w[c / 2] = pack_half2(e0, e1);
           w[c / 2 + 1] = pack_half2(e2, e3);
+        }
+        {
+          float s0, s1;
+          unpack_f2(add_f2(l2, l3), s0, s1);
+          l += (s0 + s1) * pow2i(-(int)F);
         }
         tmem_st32(S, *reinterpret_cast<uint32_t (*)[32]>(w));
         tmem_st32(S + 32, *reinterpret_cast<uint32_t (*)[32]>(w + 32));
@@ -290,10 +324,7 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, float scale_log2e, int row_
       // ---- the output, divided by the sum ----
       if (ok && started) ok = mbar_wait_warp(&o_full[g], 0, DEV_ERR_TIMEOUT_ACC);
       tc_fence_after();
-      float la, lb;
-      unpack_f2(l2, la, lb);
-      const float sum = la + lb;
-      const float inv = m == -INFINITY ? 0.f : 1.0f / sum;             // a query that sees no key: zeros
+      const float inv = m == -INFINITY ? 0.f : 0x1p-11f / l;           // a query that sees no key: zeros
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.A) + off;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
@@ -328,63 +359,79 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, float scale_log2e, int row_
       const float* vs = a.Vs + head * s.T_cap;
       uint4 kw[D / 32], vw[D / 32];
       float kstep = 0.f, vstep = 0.f;
+      const int seen_lo = a.window > 0 ? first_seen - a.window : -1;   // keys past it, and the sinks, are seen by some row
       auto load_k = [&](int i) {
         const int j = i < tiles.count ? tiles.at(i) * KP_KT + key : s.T_cap;
-        kstep = 0.f;
+        kstep = vstep = 0.f;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) kw[c] = make_uint4(0u, 0u, 0u, 0u);
-        if (j < s.T_cap) {
+        if (j <= last_seen && (j > seen_lo || j < a.sinks)) {
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) kw[c] = ldg_v4(kc + (int64_t)j * (D / 2) + 16 * c);
           kstep = ldg_f32(ks + j);
+          vstep = ldg_f32(vs + j);
         }
       };
       auto load_v = [&](int i) {
         const int j = i < tiles.count ? tiles.at(i) * KP_KT + key : s.T_cap;
-        vstep = 0.f;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) vw[c] = make_uint4(0u, 0u, 0u, 0u);
-        if (j < s.T_cap) {
+        if (j <= last_seen && (j > seen_lo || j < a.sinks)) {
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) vw[c] = ldg_v4(vc + (int64_t)j * (D / 2) + 16 * c);
-          vstep = ldg_f32(vs + j);
         }
       };
       load_k(0);
       load_v(0);
+      bool ok = true;                                // after a wait that gave up the loop only keeps its barriers
       for (int i = 0; i < tiles.count; ++i) {
         const int st = i & 1;
-        if (i >= 2 && !(mbar_wait(&k_empty[st], ((i >> 1) - 1) & 1, DEV_ERR_TIMEOUT_EMPTY) &&
-                        mbar_wait(&v_empty[st], ((i >> 1) - 1) & 1, DEV_ERR_TIMEOUT_EMPTY)))
-          break;
+        // the tile's largest steps.  A row whose steps are not finite is NaN to the queries that
+        // see it, through its key alone: a masked weight of 0 would not hide it in the values
+        const bool bad = !(fabsf(kstep) < INFINITY && fabsf(vstep) < INFINITY);
+        const uint32_t kb = bad ? 0u : __float_as_uint(fabsf(kstep)), vb = bad ? 0u : __float_as_uint(fabsf(vstep));
+        const uint32_t kt = __reduce_max_sync(0xffffffffu, kb), vt = __reduce_max_sync(0xffffffffu, vb);
+        if ((tid & 31) == 0) {
+          step_top[st][0][warp & 3] = kt;
+          step_top[st][1][warp & 3] = vt;
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        const uint4 k4 = *reinterpret_cast<const uint4*>(step_top[st][0]), v4 = *reinterpret_cast<const uint4*>(step_top[st][1]);
+        const int E = row_exponent(__uint_as_float(max(max(k4.x, k4.y), max(k4.z, k4.w))));
+        const int F = step_exponent(__uint_as_float(max(max(v4.x, v4.y), max(v4.z, v4.w))));
+        const float kx = kstep * pow2i(11 - E);
+        // 8 bits of the step times a code are exact in fp16; the rest of the step joins in one rounding
+        const float k_top = __uint_as_float(__float_as_uint(kx) & 0xFFFF0000u);
+        const uint32_t kh = bad ? 0x7FFF7FFFu : both_halves(k_top), kl = both_halves(kx - k_top);
+        const uint32_t vh = bad ? 0u : both_halves(vstep * pow2i(11 - F));
+        // the scores of tile i - 2 are complete, so both streams are done with the steps of tile i - 3
+        if (i >= 2 && ok) ok = mbar_wait(&k_empty[st], ((i >> 1) - 1) & 1, DEV_ERR_TIMEOUT_EMPTY);
         uint8_t* kd = sm + M::K + st * M::TILE + key * 128;
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {
           const uint4 q = kw[c >> 2];
           const uint32_t word = (c & 3) == 0 ? q.x : (c & 3) == 1 ? q.y : (c & 3) == 2 ? q.z : q.w;
           uint32_t v[4];
-          codes_to_bf2(word, v);
+          codes_to_half2(word, v);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = h2_fma(v[j], kl, h2_mul(v[j], kh));
           *reinterpret_cast<uint4*>(kd + (c >> 3) * 16384 + (((c & 7) ^ (key & 7)) << 4)) =
               make_uint4(v[0], v[1], v[2], v[3]);
         }
-        // steps as the streams use them: the score's factor, log2 of the value step and its
-        // reciprocal; a value step below the append's smallest is an empty row
-        const bool empty = vstep < 0x1p-24f;
-        float* sd = steps + st * 3 * KP_KT;
-        const float inv = empty ? 0x1p24f : __fdiv_rn(1.0f, vstep);
-        sd[key] = kstep * scale_log2e;
-        sd[KP_KT + key] = empty ? -24.f : log2f(vstep);
-        sd[2 * KP_KT + key] = inv == inv ? inv : 0.f;                  // a masked NaN step adds nothing to the sum
+        if (key == 0) steps[i % KP_STEPS] = make_float2(scale_log2e * pow2i(E - 11), (float)F);
         fence_proxy_async_smem();
         mbar_arrive(&k_full[st]);
         load_k(i + 1);
+        if (i >= 2 && ok) ok = mbar_wait(&v_empty[st], ((i >> 1) - 1) & 1, DEV_ERR_TIMEOUT_EMPTY);
         uint8_t* vd = sm + M::V + st * M::TILE + key * 128;
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {
           const uint4 q = vw[c >> 2];
           const uint32_t word = (c & 3) == 0 ? q.x : (c & 3) == 1 ? q.y : (c & 3) == 2 ? q.z : q.w;
           uint32_t v[4];
-          codes_to_half2(empty ? 0u : word, v);
+          codes_to_half2(word, v);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = h2_mul(v[j], vh);
           *reinterpret_cast<uint4*>(vd + (c >> 3) * 16384 + (((c & 7) ^ (key & 7)) << 4)) =
               make_uint4(v[0], v[1], v[2], v[3]);
         }
@@ -394,46 +441,61 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, float scale_log2e, int row_
       }
     } else {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-      if (warp == 12 && lane == 0 && tiles.count > 0) {
+      if (warp == 12 && tiles.count > 0) {
         // ---------------------------------------------- products
-        constexpr uint32_t ID_S = idesc_f16(128, KP_KT, true, false), ID_O = idesc_f16(128, D, false, true);
-        bool ok = mbar_wait(&q_full, 0, DEV_ERR_TIMEOUT_A);
-        int weights[2] = {0, 0};                     // weight tiles used, by stream
+        constexpr uint32_t ID_S = idesc_f16(128, KP_KT, false, false), ID_O = idesc_f16(128, D, false, true);
+        bool ok = mbar_wait_warp(&q_full, 0, DEV_ERR_TIMEOUT_A);
+        int used0 = 0, used1 = 0;                    // weight tiles used, by stream
         const uint32_t smq = smem_u32(sm + M::Q), smk = smem_u32(sm + M::K), smv = smem_u32(sm + M::V);
         for (int i = 0; i <= tiles.count && ok; ++i) {
           const bool more = i < tiles.count;
-          if (more) ok = mbar_wait(&k_full[i & 1], (i >> 1) & 1, DEV_ERR_TIMEOUT_FULL);
-          if (!ok) break;
-          for (int g = 0; g < 2 && ok; ++g) {
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
             const KpRows& rows = g == 0 ? rows0 : rows1;
-            if (i > 0 && rows.any(tiles.at(i - 1) * KP_KT, a.window, a.sinks)) {
-              ok = mbar_wait(&p_full[g], weights[g] & 1, DEV_ERR_TIMEOUT_ACC) &&
-                   mbar_wait(&v_full[(i - 1) & 1], ((i - 1) >> 1) & 1, DEV_ERR_TIMEOUT_FULL);
-              if (!ok) break;
-              tc_fence_after();
-              const uint32_t vb = smv + ((i - 1) & 1) * M::TILE;
+            int& used = g == 0 ? used0 : used1;
+            if (i > 0 && ok && rows.any(tiles.at(i - 1) * KP_KT, a.window, a.sinks)) {
+              ok = mbar_wait_warp(&p_full[g], used & 1, DEV_ERR_TIMEOUT_ACC) &&
+                   mbar_wait_warp(&v_full[(i - 1) & 1], ((i - 1) >> 1) & 1, DEV_ERR_TIMEOUT_FULL);
+              if (ok) {
+                tc_fence_after();
+                const uint32_t vb = smv + ((i - 1) & 1) * M::TILE;
+                if (elect_one()) {
 #pragma unroll
-              for (int k = 0; k < KP_KT / 16; ++k)
-                mma_f16_ts(tmem + O_COL + 128u * g, tmem + S_COL + 128u * g + 8 * k, smem_desc_mn_sw128(vb + 2048 * k, 16384),
-                           ID_O, weights[g] > 0 || k > 0);
-              ++weights[g];
+                  for (int k = 0; k < KP_KT / 16; ++k)
+                    mma_f16_ts(tmem + O_COL + 128u * g, tmem + S_COL + 128u * g + 8 * k,
+                               smem_desc_mn_sw128(vb + 2048 * k, 16384), ID_O, used > 0 || k > 0);
+                }
+                __syncwarp();
+                ++used;
+              }
             }
-            if (more && rows.any(tiles.at(i) * KP_KT, a.window, a.sinks)) {
+            // (a stream's wait also covers a tile that only the other stream sees)
+            if (more && ok) ok = mbar_wait_warp(&k_full[i & 1], (i >> 1) & 1, DEV_ERR_TIMEOUT_FULL);
+            if (more && ok && rows.any(tiles.at(i) * KP_KT, a.window, a.sinks)) {
               const uint32_t qb = smq + g * M::TILE, kb = smk + (i & 1) * M::TILE;
+              if (elect_one()) {
 #pragma unroll
-              for (int k = 0; k < D / 16; ++k)
-                mma_f16_ss(tmem + S_COL + 128u * g, smem_desc_k_sw128(qb + (k >> 2) * 16384 + (k & 3) * 32),
-                           smem_desc_k_sw128(kb + (k >> 2) * 16384 + (k & 3) * 32), ID_S, k > 0);
-              mma_commit(&s_full[g]);
+                for (int k = 0; k < D / 16; ++k)
+                  mma_f16_ss(tmem + S_COL + 128u * g, smem_desc_k_sw128(qb + (k >> 2) * 16384 + (k & 3) * 32),
+                             smem_desc_k_sw128(kb + (k >> 2) * 16384 + (k & 3) * 32), ID_S, k > 0);
+                mma_commit(&s_full[g]);
+              }
+              __syncwarp();
             }
           }
           if (!ok) break;
-          if (i > 0) mma_commit(&v_empty[(i - 1) & 1]);
-          if (more) mma_commit(&k_empty[i & 1]);
+          if (elect_one()) {
+            if (i > 0) mma_commit(&v_empty[(i - 1) & 1]);
+            if (more) mma_commit(&k_empty[i & 1]);
+          }
+          __syncwarp();
         }
         // completion of everything issued, also after a wait that gave up
-        mma_commit(&o_full[0]);
-        mma_commit(&o_full[1]);
+        if (elect_one()) {
+          mma_commit(&o_full[0]);
+          mma_commit(&o_full[1]);
+        }
+        __syncwarp();
         mbar_wait(&o_full[1], 0, DEV_ERR_TIMEOUT_ACC, false);
       }
     }
