@@ -76,7 +76,8 @@ _SIGNATURES = {
     "bitnet_kv4_read": (ctypes.c_int, [_c_void_p] * 4 + [_i64] * 3 + [_c_void_p] * 2 + [ctypes.c_int] * 2 + [_i64] +
                         [_c_void_p] * 2 + [ctypes.c_int, _c_void_p]),
     "bitnet_kv4_attention": (ctypes.c_int, [_c_void_p, ctypes.c_int] + [_c_void_p] * 4 + [_i64] * 3 + [_c_void_p] * 2 +
-                             [ctypes.c_int] * 3 + [_i64] * 4 + [_c_void_p] * 2),
+                             [ctypes.c_int] * 3 + [_i64] * 4 + [_c_void_p] * 2 + [ctypes.c_size_t, _c_void_p]),
+    "bitnet_kv4_attention_workspace_size": (ctypes.c_size_t, [ctypes.c_int] + [_i64] * 2 + [ctypes.c_int] * 3 + [_i64] * 4),
     "bitnet_device_error": (ctypes.c_int, [ctypes.POINTER(ctypes.c_int)]),
     "bitnet_measure_i8_mma": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, _c_void_p, _c_void_p,
                                              _c_void_p]),
@@ -550,13 +551,23 @@ def bitnet_kv4_read(cache: KV4Cache, B: int, L: int, t0: int, pos=None, lens=Non
     return K, V
 
 
+def bitnet_kv4_attention_workspace_size(dtype, B: int, L: int, heads: int, kv_heads: int, head_dim: int, T_cap: int,
+                                        window: int = 0, sinks: int = 0, t_max: int = 0) -> int:
+    """Bytes of workspace bitnet_kv4_attention needs for these arguments (0 for few queries)."""
+    code = {torch.float32: BITNET_F32, torch.bfloat16: BITNET_BF16}[dtype]
+    return int(lib().bitnet_kv4_attention_workspace_size(code, B, L, heads, kv_heads, head_dim, T_cap, window, sinks,
+                                                         t_max))
+
+
 def bitnet_kv4_attention(Q: torch.Tensor, cache: KV4Cache, B: int, L: int, t0: int, heads: int, window: int = 0,
-                         sinks: int = 0, t_max: int | None = None, pos=None, lens=None, A=None, stream=None):
+                         sinks: int = 0, t_max: int | None = None, pos=None, lens=None, A=None, workspace=None,
+                         stream=None):
     """Causal softmax attention of the rows Q [B*L, heads*d] (fp32 or bf16) over a
     4-bit cache; with window > 0 over the last `window` keys and the first `sinks`.
-    t_max: a bound on the positions in use plus one, for the split of the work over
-    the GPU (default: t0 + L without pos, else T_cap).  Returns A in Q's type; rows
-    of padding are left as they were (zeros where A is allocated here)."""
+    t_max: a bound on the positions in use plus one (default: t0 + L without pos, else
+    T_cap); a query past it counts as outside the cache.  workspace: uint8 scratch of
+    bitnet_kv4_attention_workspace_size bytes (allocated here by default).  Returns A in
+    Q's type; rows of padding are left as they were (zeros where A is allocated here)."""
     dev = Q.device
     if not Q.is_cuda:
         raise ValueError("Q must be a contiguous CUDA tensor")
@@ -572,9 +583,16 @@ def bitnet_kv4_attention(Q: torch.Tensor, cache: KV4Cache, B: int, L: int, t0: i
                 with torch.cuda.stream(on.stream):
                     A.zero_()
         _expect(A, "A", Q.dtype, (B * L, heads * d), dev)
+        t_max, code = min(int(t_max), T), _dtype_code(Q)
+        need = lib().bitnet_kv4_attention_workspace_size(code, B, L, heads, kv, d, T, int(window), int(sinks), t_max)
+        if workspace is None:
+            workspace = on.empty((need,), torch.uint8, dev) if need else None
+        else:
+            _expect(workspace, "workspace", torch.uint8, workspace.shape, dev)
         _check("bitnet_kv4_attention", lib().bitnet_kv4_attention(
-            _ptr(Q), _dtype_code(Q), _ptr(cache.kc), _ptr(cache.ks), _ptr(cache.vc), _ptr(cache.vs), B, L, t0, p, ln,
-            heads, kv, d, T, int(window), int(sinks), min(int(t_max), T), _ptr(A), on.ptr))
+            _ptr(Q), code, _ptr(cache.kc), _ptr(cache.ks), _ptr(cache.vc), _ptr(cache.vs), B, L, t0, p, ln,
+            heads, kv, d, T, int(window), int(sinks), t_max, _ptr(A), _ptr(workspace),
+            0 if workspace is None else workspace.numel(), on.ptr))
     return A
 
 

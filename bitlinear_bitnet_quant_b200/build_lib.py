@@ -3,8 +3,7 @@
     python -m bitlinear_bitnet_quant_b200.build_lib [--force] [--verbose]
 
 The library is compiled from csrc/*.cu with relocatable device code (the
-device error flag is shared across translation units; WHOLE_UNITS keep one of
-their own) and a static CUDA
+device error flag is shared across translation units) and a static CUDA
 runtime, so it needs only the NVIDIA driver at run time.  No fast-math: the
 quantisers rely on IEEE round-to-nearest fp32 division and square root.
 """
@@ -31,10 +30,6 @@ NVCC_FLAGS = [
     "--expt-relaxed-constexpr",
     "-I", INCLUDE, "-I", CSRC,
 ]
-
-# Units without relocatable device code: their warps share the register file
-# unevenly (setmaxnreg), which the compiler honours in whole programs only.
-WHOLE_UNITS = ("kv4_prefill.cu",)
 
 
 def nvcc_path() -> str:
@@ -68,8 +63,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
     procs = []
     for src in sources():
         obj = os.path.join(BUILD_DIR, os.path.basename(src).replace(".cu", ".o"))
-        flags = [f for f in NVCC_FLAGS if f != "-rdc=true" or os.path.basename(src) not in WHOLE_UNITS]
-        cmd = [nvcc, *flags, "-c", src, "-o", obj]
+        cmd = [nvcc, *NVCC_FLAGS, "-c", src, "-o", obj]
         if ptxas_verbose:
             cmd += ["-Xptxas", "-v"]
         if verbose:

@@ -47,8 +47,10 @@ cudaError_t run_attention(const float* Q, const float* Kc, const float* Vc, int 
 cudaError_t run_append(const KvStep& s, const AppendArgs& a, int x_bf16, int d, double base, cudaStream_t st);
 cudaError_t run_kv4_read(const KvStep& s, int kv_heads, int d, const uint8_t* Kc, const float* Ks, const uint8_t* Vc,
                          const float* Vs, void* K, void* V, int bf16, cudaStream_t st);
-cudaError_t kv4_prefill_error(int* code);
-cudaError_t run_kv4_attention(const KvStep& s, const AttnArgs& a, int bf16, int d, int64_t t_max, cudaStream_t st);
+bool kv4_prefill_applies(const KvStep& s, const AttnArgs& a, int bf16);
+size_t kv4_prefill_workspace(const KvStep& s, const AttnArgs& a, int d);
+cudaError_t run_kv4_prefill(const KvStep& s, const AttnArgs& a, int d, void* ws, size_t ws_bytes, cudaStream_t st);
+cudaError_t run_kv4_decode(const KvStep& s, const AttnArgs& a, int bf16, int d, cudaStream_t st);
 }  // namespace bitnet
 
 namespace {
@@ -412,6 +414,7 @@ static bitnet::KvStep kv_step(int64_t B, int64_t L, int64_t t0, const int32_t* p
   s.B = (int)B;
   s.L = (int)L;
   s.T_cap = (int)T_cap;
+  s.limit = (int)T_cap;
   return s;
 }
 
@@ -527,47 +530,78 @@ int bitnet_kv4_read(const uint8_t* Kc, const float* Ks, const uint8_t* Vc, const
                                           V, dtype == BITNET_BF16, static_cast<cudaStream_t>(stream)));
 }
 
-int bitnet_kv4_attention(const void* Q, int dtype, const uint8_t* Kc, const float* Ks, const uint8_t* Vc,
-                         const float* Vs, int64_t B, int64_t L, int64_t t0, const int32_t* pos, const int32_t* len,
-                         int heads, int kv_heads, int head_dim, int64_t T_cap, int64_t window, int64_t sinks,
-                         int64_t t_max, void* A, void* stream) {
+// What bitnet_kv4_attention and its workspace size check alike, and its operands.
+static int kv4_attention_shape(int dtype, int64_t B, int64_t L, int64_t t0, const int32_t* pos, int heads,
+                               int kv_heads, int head_dim, int64_t T_cap, int64_t window, int64_t sinks,
+                               int64_t t_max) {
   if (dtype != BITNET_F32 && dtype != BITNET_BF16) return BITNET_ERR_DTYPE;
   const int sh = kv_shape(B, L, t0, pos, heads, kv_heads, head_dim, T_cap);
   if (sh != BITNET_OK) return sh;
   if (T_cap % 16 != 0 || window < 0 || sinks < 0 || t_max < 0 || t_max > T_cap) return BITNET_ERR_SHAPE;
+  return BITNET_OK;
+}
+
+static bitnet::AttnArgs kv4_attention_args(int heads, int kv_heads, int64_t window, int64_t sinks) {
+  const int64_t most = int64_t(1) << 25;                  // past every position
+  bitnet::AttnArgs a = {};
+  a.heads = heads;
+  a.kv_heads = kv_heads;
+  a.window = (int)(window < most ? window : most);
+  a.sinks = (int)(sinks < most ? sinks : most);
+  return a;
+}
+
+size_t bitnet_kv4_attention_workspace_size(int dtype, int64_t B, int64_t L, int heads, int kv_heads, int head_dim,
+                                           int64_t T_cap, int64_t window, int64_t sinks, int64_t t_max) {
+  const int32_t any = 0;                                  // positions may come from the device
+  if (kv4_attention_shape(dtype, B, L, 0, &any, heads, kv_heads, head_dim, T_cap, window, sinks, t_max) != BITNET_OK)
+    return 0;
+  bitnet::KvStep s = kv_step(B, L, 0, nullptr, nullptr, T_cap);
+  if (t_max > 0) s.limit = (int)t_max;
+  const bitnet::AttnArgs a = kv4_attention_args(heads, kv_heads, window, sinks);
+  if (B == 0 || L == 0 || !bitnet::kv4_prefill_applies(s, a, dtype == BITNET_BF16)) return 0;
+  return bitnet::kv4_prefill_workspace(s, a, head_dim);
+}
+
+int bitnet_kv4_attention(const void* Q, int dtype, const uint8_t* Kc, const float* Ks, const uint8_t* Vc,
+                         const float* Vs, int64_t B, int64_t L, int64_t t0, const int32_t* pos, const int32_t* len,
+                         int heads, int kv_heads, int head_dim, int64_t T_cap, int64_t window, int64_t sinks,
+                         int64_t t_max, void* A, void* workspace, size_t workspace_bytes, void* stream) {
+  const int sh = kv4_attention_shape(dtype, B, L, t0, pos, heads, kv_heads, head_dim, T_cap, window, sinks, t_max);
+  if (sh != BITNET_OK) return sh;
   if (B == 0 || L == 0) return BITNET_OK;
   if (!Q || !Kc || !Ks || !Vc || !Vs || !A) return BITNET_ERR_NULL;
   if (!aligned16(Q) || !aligned16(Kc) || !aligned16(Ks) || !aligned16(Vc) || !aligned16(Vs) || !aligned16(A) ||
-      !aligned4(pos) || !aligned4(len))
+      !aligned16(workspace) || !aligned4(pos) || !aligned4(len))
     return BITNET_ERR_ALIGN;
-  const int d = check_device();
-  if (d != BITNET_OK) return d;
-  const int64_t most = int64_t(1) << 25;                  // past every position
-  bitnet::AttnArgs a = {};
+  bitnet::KvStep s = kv_step(B, L, t0, pos, len, T_cap);
+  if (t_max > 0) s.limit = (int)t_max;
+  bitnet::AttnArgs a = kv4_attention_args(heads, kv_heads, window, sinks);
   a.Q = Q;
   a.Kc = Kc;
   a.Ks = Ks;
   a.Vc = Vc;
   a.Vs = Vs;
   a.A = A;
-  a.heads = heads;
-  a.kv_heads = kv_heads;
-  a.window = (int)(window < most ? window : most);
-  a.sinks = (int)(sinks < most ? sinks : most);
-  return cuda_status(bitnet::run_kv4_attention(kv_step(B, L, t0, pos, len, T_cap), a, dtype == BITNET_BF16, head_dim,
-                                               t_max > 0 ? t_max : T_cap, static_cast<cudaStream_t>(stream)));
+  const bool prefill = bitnet::kv4_prefill_applies(s, a, dtype == BITNET_BF16);
+  if (prefill && (!workspace || workspace_bytes < bitnet::kv4_prefill_workspace(s, a, head_dim)))
+    return BITNET_ERR_WORKSPACE;
+  const int d = check_device();
+  if (d != BITNET_OK) return d;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return cuda_status(prefill ? bitnet::run_kv4_prefill(s, a, head_dim, workspace, workspace_bytes, st)
+                             : bitnet::run_kv4_decode(s, a, dtype == BITNET_BF16, head_dim, st));
 }
 
 int bitnet_device_error(int* code_out) {
-  int code = 0, other = 0, zero = 0;
+  int code = 0, zero = 0;
   if (cudaDeviceSynchronize() != cudaSuccess) { cudaGetLastError(); return BITNET_ERR_CUDA; }
   if (cudaMemcpyFromSymbol(&code, bitnet::g_device_error, sizeof(int)) != cudaSuccess ||
-      cudaMemcpyToSymbol(bitnet::g_device_error, &zero, sizeof(int)) != cudaSuccess ||
-      bitnet::kv4_prefill_error(&other) != cudaSuccess) {
+      cudaMemcpyToSymbol(bitnet::g_device_error, &zero, sizeof(int)) != cudaSuccess) {
     cudaGetLastError();
     return BITNET_ERR_CUDA;
   }
-  if (code_out) *code_out = code != 0 ? code : other;
+  if (code_out) *code_out = code;
   return BITNET_OK;
 }
 

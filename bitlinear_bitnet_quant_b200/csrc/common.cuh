@@ -19,11 +19,7 @@ namespace bitnet {
 // ---------------------------------------------------------------------------
 // error flag: set by a bounded wait that gave up; read by bitnet_device_error()
 // ---------------------------------------------------------------------------
-#ifdef BITNET_OWN_ERROR_FLAG
-static __device__ int g_device_error = 0;            // a unit compiled as a whole program
-#else
 extern __device__ int g_device_error;
-#endif
 
 enum DeviceError : int {
   DEV_ERR_NONE = 0,

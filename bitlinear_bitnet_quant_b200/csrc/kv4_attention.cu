@@ -107,8 +107,8 @@ kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e) {
   const int nr = n_rows - r0 < ROWS ? n_rows - r0 : ROWS;
   const int64_t p0 = kv_first_position(s, b);
   const int64_t pf = p0 + r0 / group, pl = p0 + (r0 + nr - 1) / group;
-  const int p_lo = pf < 0 ? 0 : (pf < s.T_cap ? (int)pf : s.T_cap);
-  const int p_hi = pl < 0 ? -1 : (pl < s.T_cap ? (int)pl : s.T_cap - 1);
+  const int p_lo = pf < 0 ? 0 : (pf < s.limit ? (int)pf : s.limit);
+  const int p_hi = pl < 0 ? -1 : (pl < s.limit ? (int)pl : s.limit - 1);
   KeyTiles tiles = key_tiles<KD_KT>(p_lo, p_hi, a.window, a.sinks);
   if (p_lo > p_hi) tiles.count = 0;                  // every query lies outside the cache
 
@@ -166,10 +166,10 @@ kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e) {
       unscale[n][i] = __shfl_sync(0xffffffffu, down, 4 * (2 * t + i));
       const int rc = 8 * n + 2 * t + i < nr ? 8 * n + 2 * t + i : nr - 1;
       const int64_t p = p0 + (r0 + rc) / group;
-      pos[n][i] = p >= 0 && p < s.T_cap ? (int)p : -1;
+      pos[n][i] = p >= 0 && p < s.limit ? (int)p : -1;
     }
   }
-  const bool rows_in = pf >= 0 && pl < s.T_cap;
+  const bool rows_in = pf >= 0 && pl < s.limit;
 
   const int64_t head = (int64_t)b * a.kv_heads + h;
   const uint8_t* kc = a.Kc + head * s.T_cap * (D / 2);
@@ -425,8 +425,6 @@ kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e) {
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-cudaError_t run_kv4_prefill(const KvStep& s, const AttnArgs& a, int d, cudaStream_t st);
-
 template <int D, int NT, typename XT>
 static cudaError_t launch_decode(const KvStep& s, const AttnArgs& a, int64_t t_max, cudaStream_t st) {
   constexpr int ROWS = 8 * NT;
@@ -447,18 +445,15 @@ static cudaError_t launch_decode(const KvStep& s, const AttnArgs& a, int64_t t_m
 }
 
 template <int D, typename XT>
-static cudaError_t launch_attention(const KvStep& s, const AttnArgs& a, int64_t t_max, cudaStream_t st) {
-  if constexpr (sizeof(XT) == 2) {
-    if ((int64_t)s.L * (a.heads / a.kv_heads) >= 128) return run_kv4_prefill(s, a, D, st);
-  }
-  if ((int64_t)s.L * (a.heads / a.kv_heads) <= 8) return launch_decode<D, 1, XT>(s, a, t_max, st);
-  return launch_decode<D, 2, XT>(s, a, t_max, st);
+static cudaError_t launch_attention(const KvStep& s, const AttnArgs& a, cudaStream_t st) {
+  if ((int64_t)s.L * (a.heads / a.kv_heads) <= 8) return launch_decode<D, 1, XT>(s, a, s.limit, st);
+  return launch_decode<D, 2, XT>(s, a, s.limit, st);
 }
 
-cudaError_t run_kv4_attention(const KvStep& s, const AttnArgs& a, int bf16, int d, int64_t t_max, cudaStream_t st) {
+cudaError_t run_kv4_decode(const KvStep& s, const AttnArgs& a, int bf16, int d, cudaStream_t st) {
   using bf = __nv_bfloat16;
-  if (d == 128) return bf16 ? launch_attention<128, bf>(s, a, t_max, st) : launch_attention<128, float>(s, a, t_max, st);
-  return bf16 ? launch_attention<64, bf>(s, a, t_max, st) : launch_attention<64, float>(s, a, t_max, st);
+  if (d == 128) return bf16 ? launch_attention<128, bf>(s, a, st) : launch_attention<128, float>(s, a, st);
+  return bf16 ? launch_attention<64, bf>(s, a, st) : launch_attention<64, float>(s, a, st);
 }
 
 }  // namespace bitnet

@@ -22,6 +22,7 @@ struct KvStep {
   const int32_t* len;                               // [B] or NULL (L)
   int64_t t0;
   int B, L, T_cap;
+  int limit;                                        // positions at or past it lie outside the cache (<= T_cap)
 };
 
 BN_DEV int kv_real_tokens(const KvStep& s, int b) {

@@ -1,8 +1,7 @@
 // Causal attention over the 4-bit key/value cache for many queries a key head
-// (prefill), on tcgen05.  This file is compiled as a whole program, so that its
-// warps can share the register file unevenly, and keeps its own copy of the error
-// flag.
-#define BITNET_OWN_ERROR_FLAG
+// (prefill), on tcgen05, in two kernels: the keys and values that the step sees are
+// expanded once into fp16 operands (a caller's workspace), then every block of query
+// rows streams them through the tensor cores.
 #include "kv4_common.cuh"
 
 #include <cuda_bf16.h>
@@ -10,35 +9,26 @@
 namespace bitnet {
 
 // ---------------------------------------------------------------------------
-// A block takes 256 rows (token, head of the group) of one key head as two streams
-// of 128, which share every tile of 128 keys: four warps unpack a tile from global
-// memory into 128-byte swizzled fp16 operands in shared memory (two stages), one
-// warp issues the products, and four warps a stream turn scores into weights, one
-// row a thread.
-//   scores  q (shared memory) x keys -> tensor memory, fp32
-//   weights written over the scores as fp16, the product's operand in tensor memory
-//   output  weights x values (keys as the reduction) -> tensor memory, fp32
-// While one stream's weights are computed, the other stream's products run.
+// Operands.  A tile's keys are code * step * 2^(11 - E) in fp16, E the exponent of the
+// tile's largest step, rounded once (half a step of fp16 is 2^-11 of a value, as for
+// the weights); its values the same with their exponent F.  A query row is scaled by a
+// power of two, bf16 values are then exact in fp16.  A row's score in base-2 exponents
+// is acc * c with one factor c a row and tile, and its weight carries the tile's 2^F,
+// p' = 2^(acc c + F - m): the output sums p' v 2^(11 - F) over all tiles in one scale,
+// and the softmax sum takes 2^-F once a tile.
 //
-// Operands.  A query row is scaled by a power of two (bf16 values are then exact in
-// fp16).  A tile's keys are code * step * 2^(11 - E) in fp16, E the exponent of the
-// tile's largest step, rounded once (2^-11 of a value, as the weights are); values the
-// same with E = F.  A row's score in base-2 exponents is then acc * c with one factor
-// c a row and tile, and its weight carries the tile's 2^F, p' = 2^(acc c + F - m): the
-// output sums p' v 2^(11 - F) over all tiles in one scale, and the softmax sum takes
-// 2^-F once a tile.  The running maximum m is that of acc c + F; it is moved only when
-// a row exceeds it by 2^8 (the weights then stay below 2^15), so the output in tensor
-// memory is rescaled rarely.  Steps in the softmax instead (a factor, an exponent and
-// a reciprocal a key, read from shared memory) took 3000 cycles a stream and tile.
+// The workspace holds, for every key head and tile, the two operands as the images that
+// shared memory takes (128-byte swizzle), so that a tile is one bulk copy, and c and F.
+// Expanding inside the attention kernel, by eight more warps of each block, cost as
+// many issue slots as the softmax and read the codes once a block: 4200 cycles a tile of
+// 128 keys and 256 rows.
 // ---------------------------------------------------------------------------
 constexpr int KP_KT = 128;                           // keys a tile
-constexpr int KP_STEPS = 4;                          // tiles whose steps are held: a stream may be two tiles behind
-constexpr int KP_THREADS = 512;                      // streams: warps 0-3 and 4-7; unpackers 8-11; products: warp 12
 
 template <int D>
-struct KpSmem {
-  static constexpr int TILE = 128 * D * 2;           // 128 rows of D 16-bit values
-  static constexpr int Q = 0, K = 2 * TILE, V = 4 * TILE, BYTES = 6 * TILE + 1024;   // 2 of each, + alignment
+struct KpTile {
+  static constexpr int BYTES = KP_KT * D * 2;        // keys or values of a tile
+  static constexpr int PAIR = 2 * BYTES;             // both
 };
 
 // One lane of a warp that runs as a whole.  The compiler knows the lane to be alone
@@ -78,26 +68,21 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool bf16, bool b
   return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? (1u << 16) : 0u) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(M >> 4) << 24);
 }
-// Shared-memory descriptor, 128-byte swizzle, N contiguous: 64-value column blocks
-// `block` bytes apart, groups of 8 reduction rows 1024 bytes apart.
-BN_DEV uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t block) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)((block >> 4) & 0x3FFFu) << 16;
-  d |= (uint64_t)(1024u >> 4) << 32;
-  d |= (uint64_t)1u << 46;
-  d |= (uint64_t)2u << 61;
-  return d;
+// Shared-memory descriptors (128-byte swizzle, groups of 8 rows 1024 bytes apart) as a
+// low word that a product's offset is added to and a constant high word: the warp that
+// issues the products must spend few instructions on each.  K-major operands ignore the
+// block distance; with N contiguous it is that of the 64-value column blocks.
+constexpr uint32_t KP_DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+BN_DEV uint32_t desc_lo(uint32_t saddr) { return (saddr >> 4) | ((16384u >> 4) << 16); }
+BN_DEV void mma_f16_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 da, {%1, %5};\n\t"
+               "mov.b64 db, {%2, %5};\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}"
+               :: "r"(d), "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(KP_DESC_HI) : "memory");
 }
-BN_DEV void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-               "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-               :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
-}
-BN_DEV void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-               "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-               :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+BN_DEV void mma_f16_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 db, {%2, %5};\n\t"
+               "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}"
+               :: "r"(d), "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(KP_DESC_HI) : "memory");
 }
 // Each lane reads 32 consecutive 32-bit columns of its own tensor-memory lane.
 BN_DEV void tmem_ld32(uint32_t taddr, uint32_t* v) {
@@ -119,55 +104,224 @@ BN_DEV uint32_t h2_mul(uint32_t a, uint32_t b) {
 }
 BN_DEV uint32_t both_halves(float v) { return pack_half2(v, v); }
 
-// Positions of one stream's rows, and what of a key tile they see.
+// Part of a sequence that its real queries see.
+struct KpSeen {
+  int first, last;                                   // positions of the first and last query, inside the cache
+  bool any;
+};
+BN_DEV KpSeen kp_seen(const KvStep& s, int b) {
+  const int n = kv_real_tokens(s, b);
+  const int64_t pf = kv_first_position(s, b), pl = pf + n - 1;
+  KpSeen r;
+  r.any = n > 0 && pl >= 0 && pf < s.limit;
+  r.first = pf < 0 ? 0 : (int)(pf < s.limit ? pf : s.limit - 1);
+  r.last = pl < 0 ? 0 : (int)(pl < s.limit ? pl : s.limit - 1);
+  return r;
+}
+
+// ---------------------------------------------------------------------------
+// Expansion: a block a tile and key head; four warps its keys, four its values.  Bound
+// by memory (reads D + 8 bytes a key and head, writes 4 D).
+// ---------------------------------------------------------------------------
+template <int D>
+__global__ void __launch_bounds__(256)
+kv4_expand_kernel(const KvStep s, const AttnArgs a, int head0, int slots, float scale_log2e, uint8_t* images,
+                  float2* factors) {
+  using M = KpTile<D>;
+  __shared__ __align__(16) uint32_t step_top[2][4];
+  pdl_launch_dependents();
+  pdl_wait();                                        // the cache comes from the previous kernel
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, val = warp >> 2, key = tid & 127;
+  const int head = head0 + blockIdx.y, b = head / a.kv_heads;
+  const KpSeen seen = kp_seen(s, b);
+  const KeyTiles tiles = key_tiles<KP_KT>(seen.first, seen.last, a.window, a.sinks);
+  const int slot = blockIdx.x;
+  if (!seen.any || slot >= tiles.count) return;
+  const int j0 = tiles.at(slot) * KP_KT;
+  const int seen_lo = a.window > 0 ? seen.first - a.window : -1;       // keys past it, and the sinks, are seen by some row
+  auto is_seen = [&](int j) { return j <= seen.last && (j > seen_lo || j < a.sinks); };
+  // a warp's 32 rows are one run of memory: lane i takes 16 bytes of every D / 2-byte row in turn,
+  // part i % PARTS of row i / PARTS + RPI q; step factors come from the lane whose number is the row's
+  constexpr int PARTS = D / 32, RPI = 32 / PARTS;
+  const int part = lane % PARTS, row0 = lane / PARTS, jw = j0 + (key & 96);
+  const uint8_t* codes = (val ? a.Vc : a.Kc) + (int64_t)head * s.T_cap * (D / 2);
+  uint4 cw[PARTS];
+#pragma unroll
+  for (int q = 0; q < PARTS; ++q) {
+    const int j = jw + row0 + RPI * q;
+    cw[q] = make_uint4(0u, 0u, 0u, 0u);
+    if (is_seen(j)) cw[q] = ldg_v4(codes + (int64_t)j * (D / 2) + 16 * part);
+  }
+  // the tile's largest steps.  A row whose steps are not finite is NaN to the queries that see
+  // it, through its key alone: a masked weight of 0 would not hide it in the values
+  float kstep = 0.f, vstep = 0.f;
+  if (is_seen(j0 + key)) {
+    kstep = ldg_f32(a.Ks + (int64_t)head * s.T_cap + j0 + key);
+    vstep = ldg_f32(a.Vs + (int64_t)head * s.T_cap + j0 + key);
+  }
+  const bool bad = !(fabsf(kstep) < INFINITY && fabsf(vstep) < INFINITY);
+  const uint32_t kt = __reduce_max_sync(0xffffffffu, bad ? 0u : __float_as_uint(fabsf(kstep)));
+  const uint32_t vt = __reduce_max_sync(0xffffffffu, bad ? 0u : __float_as_uint(fabsf(vstep)));
+  if (warp < 4 && lane == 0) {
+    step_top[0][warp] = kt;
+    step_top[1][warp] = vt;
+  }
+  __syncthreads();
+  const uint4 k4 = *reinterpret_cast<const uint4*>(step_top[0]), v4 = *reinterpret_cast<const uint4*>(step_top[1]);
+  const int E = row_exponent(__uint_as_float(max(max(k4.x, k4.y), max(k4.z, k4.w))));
+  const int F = step_exponent(__uint_as_float(max(max(v4.x, v4.y), max(v4.z, v4.w))));
+  const float step = val ? vstep * pow2i(11 - F) : kstep * pow2i(11 - E);
+  // 8 bits of the step times a code are exact in fp16; the rest of the step joins in one rounding
+  const float top = __uint_as_float(__float_as_uint(step) & 0xFFFF0000u);
+  const uint32_t sh = bad ? (val ? 0u : 0x7FFF7FFFu) : both_halves(top), sl = bad ? 0u : both_halves(step - top);
+  const int64_t tile = (int64_t)blockIdx.y * slots + slot;
+  uint8_t* dst = images + tile * M::PAIR + val * M::BYTES + (key & 96) * 128;
+#pragma unroll
+  for (int q = 0; q < PARTS; ++q) {
+    const int row = row0 + RPI * q;
+    const uint32_t rh = __shfl_sync(0xffffffffu, sh, row), rl = __shfl_sync(0xffffffffu, sl, row);
+    const uint32_t words[4] = {cw[q].x, cw[q].y, cw[q].z, cw[q].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint32_t v[4];
+      codes_to_half2(words[e], v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = h2_fma(v[j], rl, h2_mul(v[j], rh));
+      const int chunk = 4 * (part & 1) + e;
+      *reinterpret_cast<uint4*>(dst + (part >> 1) * 16384 + row * 128 + ((chunk ^ (row & 7)) << 4)) =
+          make_uint4(v[0], v[1], v[2], v[3]);
+    }
+  }
+  if (tid == 0) factors[tile] = make_float2(scale_log2e * pow2i(E - 11), (float)F);
+}
+
+// ---------------------------------------------------------------------------
+// Attention.  A block takes 256 rows (token, head of the group) of one key head as two
+// streams of 128: one warp copies tiles of 128 keys into shared memory (two stages), one
+// issues the products, and four warps a stream turn scores into weights, one row a
+// thread.
+//   scores  q (shared memory) x keys -> tensor memory, fp32
+//   weights written over the scores as fp16, the product's operand in tensor memory
+//   output  weights x values (keys as the reduction) -> tensor memory, fp32
+// While one stream's weights are computed, the other stream's products run; weights are
+// handed over in halves of 64 keys, so that the first half's product runs beside the
+// second half's exponentials.  The running maximum m is that of acc c + F; it is moved
+// only when a row exceeds it by 2^8 (the weights then stay below 2^15), so the output in
+// tensor memory is rescaled rarely, and a half's weights are computed with the maximum
+// so far while its own is found, and once more in the rare case.
+// ---------------------------------------------------------------------------
+constexpr int KP_HALF = 64;                          // keys whose weights are handed over at once
+constexpr int KP_THREADS = 320;                      // streams: warps 0-3 and 4-7; products: warp 8; copies: warp 9
+
+template <int D>
+struct KpSmem {
+  static constexpr int TILE = KpTile<D>::BYTES;      // 128 rows of D 16-bit values
+  static constexpr int Q = 0, K = 2 * TILE, V = 4 * TILE, BYTES = 6 * TILE + 1024;   // 2 of each, + alignment
+};
+
+// Bulk copy of `bytes` from global to this block's shared memory, counted on its barrier.
+BN_DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               :: "r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+}
+
+// Wait for a phase, as mbar_wait, for a whole warp.  The warp sleeps in the barrier's
+// own wait (up to 1 ms at a time): trying in a loop took a fifth of the issue slots.
+BN_DEV bool kp_wait(uint64_t* bar, uint32_t parity, int code, bool bail = true) {
+  bool ok = false;
+  for (int n = 0; n < 2000 && !ok; ++n) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(r) : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u) : "memory");
+    ok = r != 0;
+    if (!ok && bail && *((volatile int*)&g_device_error) != 0) break;
+  }
+  if (!ok) atomicCAS(&g_device_error, 0, code);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// Positions of one stream's rows, and what of n keys from j0 on they see.
 struct KpRows {
   int n, p_lo, p_hi;                                 // rows; first and last position inside the cache
   bool in;                                           // every row's position lies inside the cache
-  BN_DEV bool any(int j0, int window, int sinks) const {
-    return n > 0 && j0 <= p_hi && (window == 0 || j0 + KP_KT - 1 > p_lo - window || j0 < sinks);
+  BN_DEV bool any(int j0, int keys, int window, int sinks) const {
+    return n > 0 && j0 <= p_hi && (window == 0 || j0 + keys - 1 > p_lo - window || j0 < sinks);
   }
-  BN_DEV bool full(int j0, int window, int sinks) const {
-    return in && j0 + KP_KT - 1 <= p_lo && (window == 0 || j0 > p_hi - window || j0 + KP_KT <= sinks);
+  BN_DEV bool full(int j0, int keys, int window, int sinks) const {
+    return in && j0 + keys - 1 <= p_lo && (window == 0 || j0 > p_hi - window || j0 + keys <= sinks);
   }
 };
-BN_DEV KpRows kp_rows(int r0, int n_rows, int group, int64_t p0, int T_cap) {
+
+// One row's state in a stream, and the weights of 32 keys: e2 the exponentials' sums by
+// pairs, top the largest score, both of the half so far.
+struct KpRow {
+  float f, ref;                                      // exponent = score * f + ref
+  uint64_t sum[2];
+  float top[2];
+  int hi;                                            // the last column the row sees
+};
+// Waits for the loads of the next scores; what their use starts from passes through, so
+// that the compiler keeps every use behind the wait.
+BN_DEV void kp_scores_ready(KpRow& r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(r.ref), "+f"(r.top[0]), "+f"(r.top[1]), "+r"(r.hi) :: "memory");
+}
+BN_DEV void kp_weights(float (&x)[32], KpRow& r, uint32_t* w, bool masked, int j, int lo, int sk) {
+  if (masked) {                                      // columns j + c up to hi, and past lo or below sk
+#pragma unroll
+    for (int c = 0; c < 32; ++c) x[c] = j + c <= r.hi && (j + c > lo || j + c < sk) ? x[c] : -INFINITY;
+  }
+  const uint64_t f2 = pack_f2(r.f, r.f), ref2 = pack_f2(r.ref, r.ref);
+#pragma unroll
+  for (int c = 0; c < 16; ++c) {
+    float e0, e1;
+    r.top[c & 1] = max3(r.top[c & 1], x[2 * c], x[2 * c + 1]);
+    unpack_f2(fma_f2(pack_f2(x[2 * c], x[2 * c + 1]), f2, ref2), e0, e1);
+    e0 = ex2(e0);
+    e1 = ex2(e1);
+    r.sum[c & 1] = add_f2(r.sum[c & 1], pack_f2(e0, e1));
+    w[c] = pack_half2(e0, e1);
+  }
+}
+
+BN_DEV KpRows kp_rows(int r0, int n_rows, int group, int64_t p0, int limit) {
   KpRows r;
   r.n = n_rows - r0 < 0 ? 0 : (n_rows - r0 < 128 ? n_rows - r0 : 128);
   const int64_t pf = p0 + r0 / group, pl = p0 + (r0 + (r.n > 0 ? r.n : 1) - 1) / group;
-  r.in = pf >= 0 && pl < T_cap;
-  if (pl < 0 || pf >= T_cap) r.n = 0;                // no row sees a key
-  r.p_lo = pf < 0 ? 0 : (int)(pf < T_cap ? pf : T_cap - 1);
-  r.p_hi = pl < 0 ? 0 : (int)(pl < T_cap ? pl : T_cap - 1);
+  r.in = pf >= 0 && pl < limit;
+  if (pl < 0 || pf >= limit) r.n = 0;                // no row sees a key
+  r.p_lo = pf < 0 ? 0 : (int)(pf < limit ? pf : limit - 1);
+  r.p_hi = pl < 0 ? 0 : (int)(pl < limit ? pl : limit - 1);
   return r;
 }
 
 template <int D>
 __global__ void __launch_bounds__(KP_THREADS, 1)
-kv4_prefill_kernel(const KvStep s, const AttnArgs a, float scale_log2e, int row_tiles) {
+kv4_prefill_kernel(const KvStep s, const AttnArgs a, int head0, int heads_here, int row_tiles, int slots,
+                   const uint8_t* __restrict__ images, const float2* __restrict__ factors) {
   using M = KpSmem<D>;
   constexpr float BIAS = 7.f, MOVE = 8.f;
   constexpr uint32_t S_COL = 0, O_COL = 256;         // streams: + 128 g
   extern __shared__ uint8_t kp_raw[];
-  __shared__ uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2], q_full, s_full[2], p_full[2], o_full[2];
+  __shared__ uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2], q_full, s_full[2], p_full[2][2], o_done[2], all_done;
   __shared__ uint32_t tmem_sh;
-  __shared__ __align__(16) uint32_t step_top[2][2][4];        // read as 16 bytes
-  __shared__ float2 steps[KP_STEPS];                  // of a tile: the scores' factor, F
   uint8_t* sm = smem_align(kp_raw, 1024);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&k_full[i], 128);
-      mbar_init(&v_full[i], 128);
+      mbar_init(&k_full[i], 1);
+      mbar_init(&v_full[i], 1);
       mbar_init(&k_empty[i], 1);
       mbar_init(&v_empty[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
-      mbar_init(&o_full[i], 1);
+      mbar_init(&p_full[i][0], 128);
+      mbar_init(&p_full[i][1], 128);
+      mbar_init(&o_done[i], 1);
     }
     mbar_init(&q_full, 256);
+    mbar_init(&all_done, 1);
     fence_barrier_init();
   }
-  if (warp == 12) {
+  if (warp == 8) {
     tmem_alloc(&tmem_sh, 512);
     tmem_relinquish();
   }
@@ -180,23 +334,27 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, float scale_log2e, int row_
   pdl_wait();                                        // q and the cache come from the previous kernel
 
   // the longest row tiles first: blocks of the last rows see the most keys
-  const int heads_all = a.kv_heads * s.B;
-  const int rt = row_tiles - 1 - (int)(blockIdx.x / heads_all);
-  const int hb = (int)(blockIdx.x % heads_all), b = hb / a.kv_heads, h = hb - b * a.kv_heads;
+  const int rt = row_tiles - 1 - (int)(blockIdx.x / heads_here);
+  const int here = (int)(blockIdx.x % heads_here), b = (head0 + here) / a.kv_heads, h = head0 + here - b * a.kv_heads;
   const int group = a.heads / a.kv_heads;
   const int n_rows = kv_real_tokens(s, b) * group;
   const int r0 = rt * 256;
   const int64_t p0 = kv_first_position(s, b);
-  const KpRows rows0 = kp_rows(r0, n_rows, group, p0, s.T_cap), rows1 = kp_rows(r0 + 128, n_rows, group, p0, s.T_cap);
+  const KpRows rows0 = kp_rows(r0, n_rows, group, p0, s.limit), rows1 = kp_rows(r0 + 128, n_rows, group, p0, s.limit);
   KeyTiles tiles = {0, 0, 0};
   const int first_seen = rows0.n > 0 ? rows0.p_lo : rows1.p_lo, last_seen = rows1.n > 0 ? rows1.p_hi : rows0.p_hi;
   if (rows0.n > 0 || rows1.n > 0) tiles = key_tiles<KP_KT>(first_seen, last_seen, a.window, a.sinks);
-  const int64_t head = (int64_t)b * a.kv_heads + h;
+  // this block's tiles among the sequence's expanded ones
+  const KpSeen seen = kp_seen(s, b);
+  const KeyTiles all = key_tiles<KP_KT>(seen.first, seen.last, a.window, a.sinks);
+  auto slot = [&](int i) {
+    const int j = tiles.at(i);
+    return (int64_t)here * slots + (j < all.sink_tiles ? j : j - all.first + all.sink_tiles);
+  };
 
   if (r0 < n_rows) {
     if (warp < 8) {
       // ------------------------------------------------ a stream: scores to weights, one row a thread
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
       const int g = warp >> 2, row = tid & 127;
       const KpRows& rows = g == 0 ? rows0 : rows1;
       const int R = r0 + 128 * g + row;
@@ -204,7 +362,7 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, float scale_log2e, int row_
       const int tok = R / group;
       const int64_t off = (((int64_t)b * s.L + tok) * a.heads + h * group + R - tok * group) * D;
       const int64_t pr = p0 + tok;
-      const int p = real && pr >= 0 && pr < s.T_cap ? (int)pr : -1;
+      const int p = !real ? rows.p_hi : pr >= 0 && pr < s.limit ? (int)pr : -1;      // padding rows see what their tile does
       float row_scale;                               // base-2 score of an accumulator, up to the tile's factor
       {
         // the row's values, scaled, K-major with 128-byte swizzle
@@ -245,91 +403,85 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, float scale_log2e, int row_
       const uint32_t S = lanes + S_COL + 128u * g, O = lanes + O_COL + 128u * g;
       float m = -INFINITY;
       float l = 0.f;
-      bool started = false, ok = true;
-      int seen = 0;
+      bool ok = true;
+      int used = 0;                                  // tiles of this stream so far
       for (int i = 0; i < tiles.count && ok; ++i) {
         const int j0 = tiles.at(i) * KP_KT;
-        if (!rows.any(j0, a.window, a.sinks)) continue;
-        ok = mbar_wait_warp(&k_full[i & 1], (i >> 1) & 1, DEV_ERR_TIMEOUT_FULL) &&       // the tile's steps
-             mbar_wait_warp(&s_full[g], seen & 1, DEV_ERR_TIMEOUT_ACC);
-        ++seen;
+        if (!rows.any(j0, KP_KT, a.window, a.sinks)) continue;
+        const float2 st = factors[slot(i)];
+        ok = kp_wait(&s_full[g], used & 1, DEV_ERR_TIMEOUT_ACC);
         if (!ok) break;
         tc_fence_after();
-        const float2 st = steps[i % KP_STEPS];
-        const float f = st.x * row_scale, F = st.y;
-        float x[KP_KT];
-        {
-          uint32_t* xr = reinterpret_cast<uint32_t*>(x);
+        float x[2][32];                              // 32 scores at work, the next 32 on their way
+        tmem_ld32(S, reinterpret_cast<uint32_t*>(x[0]));
+        const float F = st.y, scale = pow2i(-(int)F);
+        KpRow r;
+        r.f = fmaxf(st.x * row_scale, 0x1p-126f);
+        r.ref = m == -INFINITY ? 0.f : BIAS + F - m;
+        const bool masked = !rows.full(j0, KP_KT, a.window, a.sinks);
+        r.hi = p - j0;
+        const int lo = a.window > 0 ? p - a.window - j0 : -1, sk = a.sinks - j0;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(S + 32 * c, xr + 32 * c);
-          tmem_wait_ld();
-        }
-        if (!rows.full(j0, a.window, a.sinks)) {
-          const int hi = p - j0;                                       // columns up to hi, and past lo or below sk
-          const int lo = a.window > 0 ? p - a.window - j0 : -1, sk = a.sinks - j0;
-#pragma unroll
-          for (int c = 0; c < KP_KT; ++c) x[c] = c <= hi && (c > lo || c < sk) ? x[c] : -INFINITY;
-        }
-        float mx = max3(x[0], x[1], x[2]), my = max3(x[3], x[4], x[5]);
-#pragma unroll
-        for (int c = 6; c < KP_KT - 2; c += 4) {
-          mx = max3(mx, x[c], x[c + 1]);
-          my = max3(my, x[c + 2], x[c + 3]);
-        }
-        mx = max3(mx, my, fmaxf(x[KP_KT - 2], x[KP_KT - 1])) * f + F;
-        if (__any_sync(0xffffffffu, mx > m + MOVE || (m == -INFINITY && mx != -INFINITY))) {
-          const float mn = fmaxf(m, mx);
-          const float down = m == -INFINITY ? 0.f : ex2(m - mn);
-          m = mn;
-          l *= down;
-          if (started) {                                               // this stream's products so far are complete
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[KP_HALF / 2];
+          r.sum[0] = r.sum[1] = 0;
+          r.top[0] = r.top[1] = -INFINITY;
+          kp_scores_ready(r);
+          tmem_ld32(S + KP_HALF * h + 32, reinterpret_cast<uint32_t*>(x[1]));
+          kp_weights(x[0], r, w, masked, KP_HALF * h, lo, sk);
+          kp_scores_ready(r);
+          if (h == 0) tmem_ld32(S + KP_HALF, reinterpret_cast<uint32_t*>(x[0]));
+          kp_weights(x[1], r, w + 16, masked, KP_HALF * h + 32, lo, sk);
+          const float top = fmaxf(r.top[0], r.top[1]) * r.f + F;
+          if (__any_sync(0xffffffffu, top > m + MOVE || (m == -INFINITY && top != -INFINITY))) {
+            // a row exceeds its maximum by too much (or sees its first key): move the maximum, and
+            // the half's weights once more
+            const float mn = fmaxf(m, top);
+            float down = m == -INFINITY ? 0.f : ex2(m - mn);
+            m = mn;
+            l *= down;
+            if (used > 0 || h > 0) {
+              // every product before this tile's first half was issued ahead of its scores
+              if (h > 0) ok = kp_wait(&o_done[g], used & 1, DEV_ERR_TIMEOUT_ACC);
+              if (!ok) break;
+              tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              uint32_t v[32];
-              tmem_ld32(O + c, v);
-              tmem_wait_ld();
+              for (int c = 0; c < D; c += 32) {
+                tmem_ld32(O + c, reinterpret_cast<uint32_t*>(x[1]));
+                asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(down) :: "memory");
 #pragma unroll
-              for (int q = 0; q < 32; ++q) v[q] = __float_as_uint(__uint_as_float(v[q]) * down);
-              tmem_st32(O + c, v);
+                for (int q = 0; q < 32; ++q) x[1][q] *= down;
+                tmem_st32(O + c, reinterpret_cast<uint32_t (&)[32]>(x[1]));
+              }
+            }
+            r.ref = m == -INFINITY ? 0.f : BIAS + F - m;
+            r.sum[0] = r.sum[1] = 0;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              tmem_ld32(S + KP_HALF * h + 32 * c, reinterpret_cast<uint32_t*>(x[1]));
+              kp_scores_ready(r);
+              kp_weights(x[1], r, w + 16 * c, masked, KP_HALF * h + 32 * c, lo, sk);
             }
           }
-        }
-        started = true;
-        const float ref = m == -INFINITY ? 0.f : BIAS + F - m;
-        const uint64_t ref2 = pack_f2(ref, ref), f2 = pack_f2(f, f);
-        uint64_t l2 = 0, l3 = 0;
-        uint32_t w[KP_KT / 2];
-#pragma unroll
-        for (int c = 0; c < KP_KT; c += 4) {
-          float e0, e1, e2, e3;
-          unpack_f2(fma_f2(pack_f2(x[c], x[c + 1]), f2, ref2), e0, e1);
-          unpack_f2(fma_f2(pack_f2(x[c + 2], x[c + 3]), f2, ref2), e2, e3);
-          e0 = ex2(e0); e1 = ex2(e1); e2 = ex2(e2); e3 = ex2(e3);
-          l2 = add_f2(l2, pack_f2(e0, e1));
-          l3 = add_f2(l3, pack_f2(e2, e3));
-          w[c / 2] = pack_half2(e0, e1);
-          w[c / 2 + 1] = pack_half2(e2, e3);
-        }
-        {
+          tmem_st32(S + KP_HALF / 2 * h, w);                           // over scores that have been read
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&p_full[g][h]);
           float s0, s1;
-          unpack_f2(add_f2(l2, l3), s0, s1);
-          l += (s0 + s1) * pow2i(-(int)F);
+          unpack_f2(add_f2(r.sum[0], r.sum[1]), s0, s1);
+          l += (s0 + s1) * scale;
         }
-        tmem_st32(S, *reinterpret_cast<uint32_t (*)[32]>(w));
-        tmem_st32(S + 32, *reinterpret_cast<uint32_t (*)[32]>(w + 32));
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&p_full[g]);
+        ++used;
       }
       // ---- the output, divided by the sum ----
-      if (ok && started) ok = mbar_wait_warp(&o_full[g], 0, DEV_ERR_TIMEOUT_ACC);
+      if (ok && used > 0) ok = kp_wait(&all_done, 0, DEV_ERR_TIMEOUT_ACC);
       tc_fence_after();
       const float inv = m == -INFINITY ? 0.f : 0x1p-11f / l;           // a query that sees no key: zeros
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.A) + off;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t v[32];
-        if (started) {
+        if (used > 0) {
           tmem_ld32(O + c, v);
           tmem_wait_ld();
         }
@@ -349,135 +501,66 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, float scale_log2e, int row_
         }
       }
       tc_fence_before();
-    } else if (warp < 12) {
-      // ------------------------------------------------ codes to operands: one key a thread
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-      const int key = tid & 127;
-      const uint8_t* kc = a.Kc + head * s.T_cap * (D / 2);
-      const uint8_t* vc = a.Vc + head * s.T_cap * (D / 2);
-      const float* ks = a.Ks + head * s.T_cap;
-      const float* vs = a.Vs + head * s.T_cap;
-      uint4 kw[D / 32], vw[D / 32];
-      float kstep = 0.f, vstep = 0.f;
-      const int seen_lo = a.window > 0 ? first_seen - a.window : -1;   // keys past it, and the sinks, are seen by some row
-      auto load_k = [&](int i) {
-        const int j = i < tiles.count ? tiles.at(i) * KP_KT + key : s.T_cap;
-        kstep = vstep = 0.f;
+    } else if (warp == 9) {
+      // ------------------------------------------------ copies
+      bool ok = true;
+      for (int i = 0; i < tiles.count && ok; ++i) {
+        const uint8_t* src = images + slot(i) * (2 * M::TILE);
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) kw[c] = make_uint4(0u, 0u, 0u, 0u);
-        if (j <= last_seen && (j > seen_lo || j < a.sinks)) {
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) kw[c] = ldg_v4(kc + (int64_t)j * (D / 2) + 16 * c);
-          kstep = ldg_f32(ks + j);
-          vstep = ldg_f32(vs + j);
+        for (int v = 0; v < 2; ++v) {
+          uint64_t *full = v ? &v_full[i & 1] : &k_full[i & 1], *empty = v ? &v_empty[i & 1] : &k_empty[i & 1];
+          if (i >= 2 && ok) ok = kp_wait(empty, ((i >> 1) - 1) & 1, DEV_ERR_TIMEOUT_EMPTY);
+          if (ok && elect_one()) {
+            mbar_arrive_expect_tx(full, M::TILE);
+            bulk_load(sm + (v ? M::V : M::K) + (i & 1) * M::TILE, src + v * M::TILE, M::TILE, full);
+          }
+          __syncwarp();
         }
-      };
-      auto load_v = [&](int i) {
-        const int j = i < tiles.count ? tiles.at(i) * KP_KT + key : s.T_cap;
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) vw[c] = make_uint4(0u, 0u, 0u, 0u);
-        if (j <= last_seen && (j > seen_lo || j < a.sinks)) {
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) vw[c] = ldg_v4(vc + (int64_t)j * (D / 2) + 16 * c);
-        }
-      };
-      load_k(0);
-      load_v(0);
-      bool ok = true;                                // after a wait that gave up the loop only keeps its barriers
-      for (int i = 0; i < tiles.count; ++i) {
-        const int st = i & 1;
-        // the tile's largest steps.  A row whose steps are not finite is NaN to the queries that
-        // see it, through its key alone: a masked weight of 0 would not hide it in the values
-        const bool bad = !(fabsf(kstep) < INFINITY && fabsf(vstep) < INFINITY);
-        const uint32_t kb = bad ? 0u : __float_as_uint(fabsf(kstep)), vb = bad ? 0u : __float_as_uint(fabsf(vstep));
-        const uint32_t kt = __reduce_max_sync(0xffffffffu, kb), vt = __reduce_max_sync(0xffffffffu, vb);
-        if ((tid & 31) == 0) {
-          step_top[st][0][warp & 3] = kt;
-          step_top[st][1][warp & 3] = vt;
-        }
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        const uint4 k4 = *reinterpret_cast<const uint4*>(step_top[st][0]), v4 = *reinterpret_cast<const uint4*>(step_top[st][1]);
-        const int E = row_exponent(__uint_as_float(max(max(k4.x, k4.y), max(k4.z, k4.w))));
-        const int F = step_exponent(__uint_as_float(max(max(v4.x, v4.y), max(v4.z, v4.w))));
-        const float kx = kstep * pow2i(11 - E);
-        // 8 bits of the step times a code are exact in fp16; the rest of the step joins in one rounding
-        const float k_top = __uint_as_float(__float_as_uint(kx) & 0xFFFF0000u);
-        const uint32_t kh = bad ? 0x7FFF7FFFu : both_halves(k_top), kl = both_halves(kx - k_top);
-        const uint32_t vh = bad ? 0u : both_halves(vstep * pow2i(11 - F));
-        // the scores of tile i - 2 are complete, so both streams are done with the steps of tile i - 3
-        if (i >= 2 && ok) ok = mbar_wait(&k_empty[st], ((i >> 1) - 1) & 1, DEV_ERR_TIMEOUT_EMPTY);
-        uint8_t* kd = sm + M::K + st * M::TILE + key * 128;
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 q = kw[c >> 2];
-          const uint32_t word = (c & 3) == 0 ? q.x : (c & 3) == 1 ? q.y : (c & 3) == 2 ? q.z : q.w;
-          uint32_t v[4];
-          codes_to_half2(word, v);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] = h2_fma(v[j], kl, h2_mul(v[j], kh));
-          *reinterpret_cast<uint4*>(kd + (c >> 3) * 16384 + (((c & 7) ^ (key & 7)) << 4)) =
-              make_uint4(v[0], v[1], v[2], v[3]);
-        }
-        if (key == 0) steps[i % KP_STEPS] = make_float2(scale_log2e * pow2i(E - 11), (float)F);
-        fence_proxy_async_smem();
-        mbar_arrive(&k_full[st]);
-        load_k(i + 1);
-        if (i >= 2 && ok) ok = mbar_wait(&v_empty[st], ((i >> 1) - 1) & 1, DEV_ERR_TIMEOUT_EMPTY);
-        uint8_t* vd = sm + M::V + st * M::TILE + key * 128;
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 q = vw[c >> 2];
-          const uint32_t word = (c & 3) == 0 ? q.x : (c & 3) == 1 ? q.y : (c & 3) == 2 ? q.z : q.w;
-          uint32_t v[4];
-          codes_to_half2(word, v);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] = h2_mul(v[j], vh);
-          *reinterpret_cast<uint4*>(vd + (c >> 3) * 16384 + (((c & 7) ^ (key & 7)) << 4)) =
-              make_uint4(v[0], v[1], v[2], v[3]);
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(&v_full[st]);
-        load_v(i + 1);
       }
     } else {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-      if (warp == 12 && tiles.count > 0) {
+      if (warp == 8 && tiles.count > 0) {
         // ---------------------------------------------- products
         constexpr uint32_t ID_S = idesc_f16(128, KP_KT, false, false), ID_O = idesc_f16(128, D, false, true);
-        bool ok = mbar_wait_warp(&q_full, 0, DEV_ERR_TIMEOUT_A);
-        int used0 = 0, used1 = 0;                    // weight tiles used, by stream
-        const uint32_t smq = smem_u32(sm + M::Q), smk = smem_u32(sm + M::K), smv = smem_u32(sm + M::V);
+        bool ok = kp_wait(&q_full, 0, DEV_ERR_TIMEOUT_A);
+        const uint32_t qd = desc_lo(smem_u32(sm + M::Q)), kd = desc_lo(smem_u32(sm + M::K)), vd = desc_lo(smem_u32(sm + M::V));
+        int used0 = 0, used1 = 0;                    // tiles used, by stream
+        bool was0 = false, was1 = false;             // the last tile was one of the stream's
         for (int i = 0; i <= tiles.count && ok; ++i) {
           const bool more = i < tiles.count;
+          const int j0 = more ? tiles.at(i) * KP_KT : 0;
+          const uint32_t kb = kd + (i & 1) * (M::TILE >> 4), vb = vd + ((i - 1) & 1) * (M::TILE >> 4);
+          if (i > 0) ok = kp_wait(&v_full[(i - 1) & 1], ((i - 1) >> 1) & 1, DEV_ERR_TIMEOUT_FULL);
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
-            const KpRows& rows = g == 0 ? rows0 : rows1;
             int& used = g == 0 ? used0 : used1;
-            if (i > 0 && ok && rows.any(tiles.at(i - 1) * KP_KT, a.window, a.sinks)) {
-              ok = mbar_wait_warp(&p_full[g], used & 1, DEV_ERR_TIMEOUT_ACC) &&
-                   mbar_wait_warp(&v_full[(i - 1) & 1], ((i - 1) >> 1) & 1, DEV_ERR_TIMEOUT_FULL);
-              if (ok) {
-                tc_fence_after();
-                const uint32_t vb = smv + ((i - 1) & 1) * M::TILE;
-                if (elect_one()) {
+            bool& was = g == 0 ? was0 : was1;
+            if (was) {
 #pragma unroll
-                  for (int k = 0; k < KP_KT / 16; ++k)
-                    mma_f16_ts(tmem + O_COL + 128u * g, tmem + S_COL + 128u * g + 8 * k,
-                               smem_desc_mn_sw128(vb + 2048 * k, 16384), ID_O, used > 0 || k > 0);
+              for (int h = 0; h < 2; ++h) {
+                if (ok) ok = kp_wait(&p_full[g][h], used & 1, DEV_ERR_TIMEOUT_ACC);
+                if (ok) {
+                  tc_fence_after();
+                  if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < KP_HALF / 16; ++k)
+                      mma_f16_ts(tmem + O_COL + 128u * g, tmem + S_COL + 128u * g + KP_HALF / 2 * h + 8 * k,
+                                 vb + h * (KP_HALF * 128 >> 4) + (2048 >> 4) * k, ID_O, h > 0 || k > 0 ? 1u : (uint32_t)used);
+                    if (h == 0) mma_commit(&o_done[g]);
+                  }
+                  __syncwarp();
                 }
-                __syncwarp();
-                ++used;
               }
+              ++used;
             }
+            was = more && (g == 0 ? rows0 : rows1).any(j0, KP_KT, a.window, a.sinks);
             // (a stream's wait also covers a tile that only the other stream sees)
-            if (more && ok) ok = mbar_wait_warp(&k_full[i & 1], (i >> 1) & 1, DEV_ERR_TIMEOUT_FULL);
-            if (more && ok && rows.any(tiles.at(i) * KP_KT, a.window, a.sinks)) {
-              const uint32_t qb = smq + g * M::TILE, kb = smk + (i & 1) * M::TILE;
+            if (more && ok) ok = kp_wait(&k_full[i & 1], (i >> 1) & 1, DEV_ERR_TIMEOUT_FULL);
+            if (was && ok) {
               if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                  mma_f16_ss(tmem + S_COL + 128u * g, smem_desc_k_sw128(qb + (k >> 2) * 16384 + (k & 3) * 32),
-                             smem_desc_k_sw128(kb + (k >> 2) * 16384 + (k & 3) * 32), ID_S, k > 0);
+                  mma_f16_ss(tmem + S_COL + 128u * g, qd + g * (M::TILE >> 4) + ((k >> 2) * 16384 + (k & 3) * 32 >> 4),
+                             kb + ((k >> 2) * 16384 + (k & 3) * 32 >> 4), ID_S, k > 0);
                 mma_commit(&s_full[g]);
               }
               __syncwarp();
@@ -491,17 +574,14 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, float scale_log2e, int row_
           __syncwarp();
         }
         // completion of everything issued, also after a wait that gave up
-        if (elect_one()) {
-          mma_commit(&o_full[0]);
-          mma_commit(&o_full[1]);
-        }
+        if (elect_one()) mma_commit(&all_done);
         __syncwarp();
-        mbar_wait(&o_full[1], 0, DEV_ERR_TIMEOUT_ACC, false);
+        mbar_wait(&all_done, 0, DEV_ERR_TIMEOUT_ACC, false);
       }
     }
   }
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 8) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -510,26 +590,58 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, float scale_log2e, int row_
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
+// Tiles of a sequence that a step's queries can see, at most.
+static int64_t kp_slots(const KvStep& s, const AttnArgs& a) {
+  const int64_t all = ((int64_t)s.limit + KP_KT - 1) / KP_KT;
+  if (a.window == 0) return all;
+  const int64_t some = ((int64_t)a.sinks + KP_KT - 1) / KP_KT + ((int64_t)a.window + s.L + KP_KT - 1) / KP_KT + 1;
+  return some < all ? some : all;
+}
+// Workspace of one key head: its tiles' images, then their factors (both in multiples of 16 bytes).
+static int64_t kp_head_bytes(const KvStep& s, const AttnArgs& a, int d) {
+  return kp_slots(s, a) * (2 * KP_KT * d * 2 + 16);
+}
+// Enough for one launch of every head, or 256 MB: heads are then taken in turns.
+size_t kv4_prefill_workspace(const KvStep& s, const AttnArgs& a, int d) {
+  const int64_t head = kp_head_bytes(s, a, d), heads = (int64_t)a.kv_heads * s.B, most = (int64_t)256 << 20;
+  int64_t turn = most / head;
+  turn = turn < 1 ? 1 : (turn < heads ? turn : heads);
+  return (size_t)(turn * head);
+}
+
 template <int D>
-static cudaError_t launch_prefill(const KvStep& s, const AttnArgs& a, cudaStream_t st) {
+static cudaError_t launch_prefill(const KvStep& s, const AttnArgs& a, uint8_t* ws, size_t ws_bytes, cudaStream_t st) {
   auto kern = kv4_prefill_kernel<D>;
   constexpr size_t smem = KpSmem<D>::BYTES;
-  const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), smem);
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   const int row_tiles = (int)(((int64_t)s.L * (a.heads / a.kv_heads) + 255) / 256);
-  return launch_pdl(kern, dim3((unsigned)(row_tiles * a.kv_heads * s.B)), dim3(KP_THREADS), smem, st, 1u, s, a,
-                    (float)(1.4426950408889634 / sqrt((double)D)), row_tiles);
+  const int slots = (int)kp_slots(s, a), heads = a.kv_heads * s.B;
+  const int64_t fit = (int64_t)ws_bytes / kp_head_bytes(s, a, D);
+  const int most = heads < 65535 ? heads : 65535;            // a grid dimension
+  const int turn = (int)(fit < most ? fit : most);
+  if (turn < 1) return cudaErrorInvalidValue;
+  float2* factors = reinterpret_cast<float2*>(ws + (int64_t)turn * slots * KpTile<D>::PAIR);
+  for (int head0 = 0; head0 < heads; head0 += turn) {
+    const int n = heads - head0 < turn ? heads - head0 : turn;
+    e = launch_pdl(kv4_expand_kernel<D>, dim3((unsigned)slots, (unsigned)n), dim3(256), 0, st, 1u, s, a, head0, slots,
+                   (float)(1.4426950408889634 / sqrt((double)D)), ws, factors);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(kern, dim3((unsigned)(row_tiles * n)), dim3(KP_THREADS), smem, st, 1u, s, a, head0, n, row_tiles,
+                   slots, (const uint8_t*)ws, (const float2*)factors);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
-cudaError_t run_kv4_prefill(const KvStep& s, const AttnArgs& a, int d, cudaStream_t st) {
-  return d == 128 ? launch_prefill<128>(s, a, st) : launch_prefill<64>(s, a, st);
+// Whether the step takes this path (the others need no workspace).
+bool kv4_prefill_applies(const KvStep& s, const AttnArgs& a, int bf16) {
+  return bf16 && (int64_t)s.L * (a.heads / a.kv_heads) >= 128;
 }
 
-// Reads and clears this unit's error flag on the current device.
-cudaError_t kv4_prefill_error(int* code) {
-  int zero = 0;
-  const cudaError_t e = cudaMemcpyFromSymbol(code, g_device_error, sizeof(int));
-  return e != cudaSuccess ? e : cudaMemcpyToSymbol(g_device_error, &zero, sizeof(int));
+cudaError_t run_kv4_prefill(const KvStep& s, const AttnArgs& a, int d, void* ws, size_t ws_bytes, cudaStream_t st) {
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  return d == 128 ? launch_prefill<128>(s, a, w, ws_bytes, st) : launch_prefill<64>(s, a, w, ws_bytes, st);
 }
 
 }  // namespace bitnet

@@ -408,8 +408,14 @@ BITNET_API int bitnet_kv4_read(const uint8_t* Kc, const float* Ks, const uint8_t
  *   writes them (0, or 1e-5 / 7 and more; below 2^60).
  * Q, A   : [B*L][heads*d] in dtype (A may be Q itself).
  * window : 0 (every key) or the number of keys of the window; sinks >= 0.
- * t_max  : a bound on the positions in use plus one, 1 .. T_cap, or 0 (T_cap).  It
- *          only steers how the work is split over the GPU.
+ * t_max  : a bound on the positions in use plus one, 1 .. T_cap, or 0 (T_cap): a
+ *          query at or past it counts as outside the cache.  The work is split, and
+ *          the workspace sized, for it.
+ * workspace: device scratch, 16-byte aligned, of at least
+ *          bitnet_kv4_attention_workspace_size bytes for the same arguments (0: not
+ *          read; steps of few queries need none, others up to 256 MB, or one key head's
+ *          share where that is more), overwritten.  Two calls that may run at the same
+ *          time, captured ones among them, need one each.
  * fp32 softmax; products with fp16 operands that hold the codes exactly, bf16
  * queries to 11 bits and more and fp32 queries to 22 bits, and the weights to 11
  * (bf16) or 22 bits (fp32).
@@ -417,7 +423,11 @@ BITNET_API int bitnet_kv4_read(const uint8_t* Kc, const float* Ks, const uint8_t
 BITNET_API int bitnet_kv4_attention(const void* Q, int dtype, const uint8_t* Kc, const float* Ks, const uint8_t* Vc,
                                     const float* Vs, int64_t B, int64_t L, int64_t t0, const int32_t* pos,
                                     const int32_t* len, int heads, int kv_heads, int head_dim, int64_t T_cap,
-                                    int64_t window, int64_t sinks, int64_t t_max, void* A, void* stream);
+                                    int64_t window, int64_t sinks, int64_t t_max, void* A, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+BITNET_API size_t bitnet_kv4_attention_workspace_size(int dtype, int64_t B, int64_t L, int heads, int kv_heads,
+                                                      int head_dim, int64_t T_cap, int64_t window, int64_t sinks,
+                                                      int64_t t_max);
 
 /*
  * Reads and clears the library's device-side error flag on the current

@@ -75,10 +75,10 @@ def test_read_and_attention_refusals(lib):
                                  a["kv"], a["d"], a["T"], a["K"], a["V"], a["dt"], None)
 
     def at(**kw):
-        a = _rows(**dict(dict(dt=0, w=0, s=0, tm=0, A=0x30000), **kw))
+        a = _rows(**dict(dict(dt=0, w=0, s=0, tm=0, A=0x30000, ws=None, wsb=0), **kw))
         return lib.bitnet_kv4_attention(a["Q"], a["dt"], a["Kc"], a["Ks"], a["Vc"], a["Vs"], a["B"], a["L"], a["t0"],
                                       a["pos"], a["len"], a["heads"], a["kv"], a["d"], a["T"], a["w"], a["s"],
-                                      a["tm"], a["A"], None)
+                                      a["tm"], a["A"], a["ws"], a["wsb"], None)
     for call in (rd, at):
         assert call(dt=2) == 4
         for bad in (dict(d=32), dict(kv=0), dict(B=-1), dict(L=-1), dict(t0=-1), dict(t0=62), dict(T=72), dict(T=0)):
@@ -89,7 +89,17 @@ def test_read_and_attention_refusals(lib):
         assert call(pos=A16 + 1) == 3
     assert rd(K=None, V=None) == 1 and rd(K=BAD) == 3
     assert at(heads=3, kv=2) == 2 and at(w=-1) == 2 and at(s=-1) == 2 and at(tm=65) == 2 and at(tm=-1) == 2
-    assert at(Q=None) == 1 and at(A=None) == 1 and at(A=BAD) == 3
+    assert at(Q=None) == 1 and at(A=None) == 1 and at(A=BAD) == 3 and at(ws=BAD) == 3
+    size = lambda dt, L, T=4096, w=0, s=0, tm=0, d=128, B=2: lib.bitnet_kv4_attention_workspace_size(
+        dt, B, L, 8, 2, d, T, w, s, tm)
+    assert size(1, 1) == 0 and size(2, 512) == 0 and size(1, 512, d=32) == 0 and size(1, 512, B=0) == 0
+    need = size(1, 512)
+    assert need == 4 * 32 * (65536 + 16)                                  # 4 heads, 32 tiles of 128 keys
+    assert size(1, 512, tm=1000) == 4 * 8 * (65536 + 16) and size(1, 512, w=100, s=4) == 4 * 7 * (65536 + 16)
+    assert size(1, 512, T=1 << 24) == (1 << 17) * (65536 + 16)            # one head's share
+    assert size(1, 512, B=4096, d=64) <= 256 << 20
+    big = dict(dt=1, B=2, L=512, heads=8, kv=2, T=4096)
+    assert at(**big) == 7 and at(ws=0x50000, wsb=need - 1, **big) == 7
 
 
 def test_binding_refuses_host_tensors():
