@@ -24,6 +24,9 @@ namespace bitnet {
 // 128 keys and 256 rows.
 // ---------------------------------------------------------------------------
 constexpr int KP_KT = 128;                           // keys a tile
+constexpr int KP_POLY = 4;                           // every KP_POLY-th pair's exponentials run on the multiply-add units
+// 2^r on [-1/2, 1/2], the cubic of least largest relative error (7.5e-05), by linear programming
+constexpr float EXP2_C0 = 0.999928073f, EXP2_C1 = 0.693260985f, EXP2_C2 = 0.242611125f, EXP2_C3 = 0.055171670f;
 
 template <int D>
 struct KpTile {
@@ -203,14 +206,13 @@ kv4_expand_kernel(const KvStep s, const AttnArgs a, int head0, int slots, float 
 //   scores  q (shared memory) x keys -> tensor memory, fp32
 //   weights written over the scores as fp16, the product's operand in tensor memory
 //   output  weights x values (keys as the reduction) -> tensor memory, fp32
-// While one stream's weights are computed, the other stream's products run; weights are
-// handed over in halves of 64 keys, so that the first half's product runs beside the
-// second half's exponentials.  The running maximum m is that of acc c + F; it is moved
+// While one stream's weights are computed, the other stream's products run.  A row's 128
+// scores are worked on at once, from one load: in parts of 32 or 64 the special-function
+// units ran dry at every part's ends.  The running maximum m is that of acc c + F; it is moved
 // only when a row exceeds it by 2^8 (the weights then stay below 2^15), so the output in
-// tensor memory is rescaled rarely, and a half's weights are computed with the maximum
+// tensor memory is rescaled rarely, and a tile's weights are computed with the maximum
 // so far while its own is found, and once more in the rare case.
 // ---------------------------------------------------------------------------
-constexpr int KP_HALF = 64;                          // keys whose weights are handed over at once
 constexpr int KP_THREADS = 320;                      // streams: warps 0-3 and 4-7; products: warp 8; copies: warp 9
 
 template <int D>
@@ -225,18 +227,12 @@ BN_DEV void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar)
                :: "r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
 }
 
-// Wait for a phase, as mbar_wait, for a whole warp.  The warp sleeps in the barrier's
-// own wait (up to 1 ms at a time): trying in a loop took a fifth of the issue slots.
-BN_DEV bool kp_wait(uint64_t* bar, uint32_t parity, int code, bool bail = true) {
+// Wait for a phase, as mbar_wait, for a whole warp; the clock is looked at only after
+// many tries (reading it takes longer than most waits here).
+BN_DEV bool kp_wait(uint64_t* bar, uint32_t parity, int code) {
   bool ok = false;
-  for (int n = 0; n < 2000 && !ok; ++n) {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(r) : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u) : "memory");
-    ok = r != 0;
-    if (!ok && bail && *((volatile int*)&g_device_error) != 0) break;
-  }
-  if (!ok) atomicCAS(&g_device_error, 0, code);
+  for (int n = 0; n < 1024 && !ok; ++n) ok = mbar_try_wait(bar, parity);
+  if (!ok) ok = mbar_wait(bar, parity, code);
   return __all_sync(0xffffffffu, ok);
 }
 
@@ -252,35 +248,60 @@ struct KpRows {
   }
 };
 
-// One row's state in a stream, and the weights of 32 keys: e2 the exponentials' sums by
-// pairs, top the largest score, both of the half so far.
-struct KpRow {
-  float f, ref;                                      // exponent = score * f + ref
-  uint64_t sum[2];
-  float top[2];
-  int hi;                                            // the last column the row sees
-};
-// Waits for the loads of the next scores; what their use starts from passes through, so
-// that the compiler keeps every use behind the wait.
-BN_DEV void kp_scores_ready(KpRow& r) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(r.ref), "+f"(r.top[0]), "+f"(r.top[1]), "+r"(r.hi) :: "memory");
+// 2^x of a pair on the multiply-add units: x = n + r with r in [-1/2, 1/2] by adding
+// 1.5 * 2^23, a cubic for 2^r (relative error 1e-4, a fifth of the fp16 rounding that
+// follows), and n into the exponent.  x below -125 counts as -125 (2^-125 rounds to
+// zero in fp16).
+BN_DEV void exp2_pair(uint64_t x, float& e0, float& e1) {
+  float a, b;
+  unpack_f2(x, a, b);
+  const uint64_t v = pack_f2(fmaxf(a, -125.f), fmaxf(b, -125.f));
+  const uint64_t big = pack_f2(12582912.f, 12582912.f), nbig = pack_f2(-12582912.f, -12582912.f);
+  const uint64_t t = add_f2(v, big);
+  const uint64_t n = add_f2(t, nbig);
+  const uint64_t r = fma_f2(n, pack_f2(-1.f, -1.f), v);
+  uint64_t q = fma_f2(pack_f2(EXP2_C3, EXP2_C3), r, pack_f2(EXP2_C2, EXP2_C2));
+  q = fma_f2(q, r, pack_f2(EXP2_C1, EXP2_C1));
+  q = fma_f2(q, r, pack_f2(EXP2_C0, EXP2_C0));
+  float t0, t1, q0, q1;
+  unpack_f2(t, t0, t1);
+  unpack_f2(q, q0, q1);
+  e0 = __uint_as_float(__float_as_uint(q0) + (__float_as_uint(t0) << 23));
+  e1 = __uint_as_float(__float_as_uint(q1) + (__float_as_uint(t1) << 23));
 }
-BN_DEV void kp_weights(float (&x)[32], KpRow& r, uint32_t* w, bool masked, int j, int lo, int sk) {
-  if (masked) {                                      // columns j + c up to hi, and past lo or below sk
+
+// The weights of a tile's keys for one row, as fp16 pairs, for exponents x f + ref; their
+// sum and the largest score go out.  Every KP_POLY-th pair's exponentials come from the
+// multiply-add units: the special-function units alone would take 2048 cycles a tile.
+BN_DEV void kp_weights(const float (&x)[KP_KT], float f, float ref, uint32_t (&w)[KP_KT / 2], float& sum, float& top) {
+  const uint64_t f2 = pack_f2(f, f), ref2 = pack_f2(ref, ref);
+  uint64_t s2[4] = {0, 0, 0, 0};
+  float mx[4] = {x[0], x[2], x[4], x[6]};
 #pragma unroll
-    for (int c = 0; c < 32; ++c) x[c] = j + c <= r.hi && (j + c > lo || j + c < sk) ? x[c] : -INFINITY;
-  }
-  const uint64_t f2 = pack_f2(r.f, r.f), ref2 = pack_f2(r.ref, r.ref);
-#pragma unroll
-  for (int c = 0; c < 16; ++c) {
+  for (int c = 0; c < KP_KT / 2; ++c) {
     float e0, e1;
-    r.top[c & 1] = max3(r.top[c & 1], x[2 * c], x[2 * c + 1]);
-    unpack_f2(fma_f2(pack_f2(x[2 * c], x[2 * c + 1]), f2, ref2), e0, e1);
-    e0 = ex2(e0);
-    e1 = ex2(e1);
-    r.sum[c & 1] = add_f2(r.sum[c & 1], pack_f2(e0, e1));
+    mx[c & 3] = max3(mx[c & 3], x[2 * c], x[2 * c + 1]);
+    const uint64_t y = fma_f2(pack_f2(x[2 * c], x[2 * c + 1]), f2, ref2);
+    if (c % KP_POLY == KP_POLY - 1) {
+      exp2_pair(y, e0, e1);
+    } else {
+      unpack_f2(y, e0, e1);
+      e0 = ex2(e0);
+      e1 = ex2(e1);
+    }
+    s2[c & 3] = add_f2(s2[c & 3], pack_f2(e0, e1));
     w[c] = pack_half2(e0, e1);
   }
+  float s0, s1;
+  unpack_f2(add_f2(add_f2(s2[0], s2[1]), add_f2(s2[2], s2[3])), s0, s1);
+  sum = s0 + s1;
+  top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+}
+
+// Completion of this warp's tensor-memory loads; what their use starts from passes
+// through, so that the compiler keeps every use behind the wait.
+BN_DEV void kp_loads_done(float& ref, float& f) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(ref), "+f"(f) :: "memory");
 }
 
 BN_DEV KpRows kp_rows(int r0, int n_rows, int group, int64_t p0, int limit) {
@@ -302,7 +323,7 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, int head0, int heads_here, 
   constexpr float BIAS = 7.f, MOVE = 8.f;
   constexpr uint32_t S_COL = 0, O_COL = 256;         // streams: + 128 g
   extern __shared__ uint8_t kp_raw[];
-  __shared__ uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2], q_full, s_full[2], p_full[2][2], o_done[2], all_done;
+  __shared__ uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2], q_full, s_full[2], p_full[2], all_done;
   __shared__ uint32_t tmem_sh;
   uint8_t* sm = smem_align(kp_raw, 1024);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -313,9 +334,7 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, int head0, int heads_here, 
       mbar_init(&k_empty[i], 1);
       mbar_init(&v_empty[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i][0], 128);
-      mbar_init(&p_full[i][1], 128);
-      mbar_init(&o_done[i], 1);
+      mbar_init(&p_full[i], 128);
     }
     mbar_init(&q_full, 256);
     mbar_init(&all_done, 1);
@@ -412,65 +431,49 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, int head0, int heads_here, 
         ok = kp_wait(&s_full[g], used & 1, DEV_ERR_TIMEOUT_ACC);
         if (!ok) break;
         tc_fence_after();
-        float x[2][32];                              // 32 scores at work, the next 32 on their way
-        tmem_ld32(S, reinterpret_cast<uint32_t*>(x[0]));
-        const float F = st.y, scale = pow2i(-(int)F);
-        KpRow r;
-        r.f = fmaxf(st.x * row_scale, 0x1p-126f);
-        r.ref = m == -INFINITY ? 0.f : BIAS + F - m;
-        const bool masked = !rows.full(j0, KP_KT, a.window, a.sinks);
-        r.hi = p - j0;
-        const int lo = a.window > 0 ? p - a.window - j0 : -1, sk = a.sinks - j0;
+        const float F = st.y;
+        float f = fmaxf(st.x * row_scale, 0x1p-126f);
+        const bool full = rows.full(j0, KP_KT, a.window, a.sinks);
+        uint32_t w[KP_KT / 2];
+        float sum, top;
+        while (true) {
+          float x[KP_KT];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w[KP_HALF / 2];
-          r.sum[0] = r.sum[1] = 0;
-          r.top[0] = r.top[1] = -INFINITY;
-          kp_scores_ready(r);
-          tmem_ld32(S + KP_HALF * h + 32, reinterpret_cast<uint32_t*>(x[1]));
-          kp_weights(x[0], r, w, masked, KP_HALF * h, lo, sk);
-          kp_scores_ready(r);
-          if (h == 0) tmem_ld32(S + KP_HALF, reinterpret_cast<uint32_t*>(x[0]));
-          kp_weights(x[1], r, w + 16, masked, KP_HALF * h + 32, lo, sk);
-          const float top = fmaxf(r.top[0], r.top[1]) * r.f + F;
-          if (__any_sync(0xffffffffu, top > m + MOVE || (m == -INFINITY && top != -INFINITY))) {
-            // a row exceeds its maximum by too much (or sees its first key): move the maximum, and
-            // the half's weights once more
-            const float mn = fmaxf(m, top);
-            float down = m == -INFINITY ? 0.f : ex2(m - mn);
-            m = mn;
-            l *= down;
-            if (used > 0 || h > 0) {
-              // every product before this tile's first half was issued ahead of its scores
-              if (h > 0) ok = kp_wait(&o_done[g], used & 1, DEV_ERR_TIMEOUT_ACC);
-              if (!ok) break;
-              tc_fence_after();
+          for (int c = 0; c < 4; ++c) tmem_ld32(S + 32 * c, reinterpret_cast<uint32_t*>(x) + 32 * c);
+          float ref = m == -INFINITY ? 0.f : BIAS + F - m;
+          kp_loads_done(ref, f);
+          if (!full) {
+            const int hi = p - j0;                                     // columns up to hi, and past lo or below sk
+            const int lo = a.window > 0 ? p - a.window - j0 : -1, sk = a.sinks - j0;
+#pragma unroll
+            for (int c = 0; c < KP_KT; ++c) x[c] = c <= hi && (c > lo || c < sk) ? x[c] : -INFINITY;
+          }
+          kp_weights(x, f, ref, w, sum, top);
+          top = top * f + F;
+          if (!__any_sync(0xffffffffu, top > m + MOVE || (m == -INFINITY && top != -INFINITY))) break;
+          // a row exceeds its maximum by too much (or sees its first key): move the maximum
+          const float mn = fmaxf(m, top);
+          float down = m == -INFINITY ? 0.f : ex2(m - mn);
+          m = mn;
+          l *= down;
+          if (used > 0) {                                              // every product so far was issued ahead of these scores
 #pragma unroll 1
-              for (int c = 0; c < D; c += 32) {
-                tmem_ld32(O + c, reinterpret_cast<uint32_t*>(x[1]));
-                asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(down) :: "memory");
+            for (int c = 0; c < D; c += 32) {
+              float v[32];
+              tmem_ld32(O + c, reinterpret_cast<uint32_t*>(v));
+              kp_loads_done(down, ref);
 #pragma unroll
-                for (int q = 0; q < 32; ++q) x[1][q] *= down;
-                tmem_st32(O + c, reinterpret_cast<uint32_t (&)[32]>(x[1]));
-              }
-            }
-            r.ref = m == -INFINITY ? 0.f : BIAS + F - m;
-            r.sum[0] = r.sum[1] = 0;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              tmem_ld32(S + KP_HALF * h + 32 * c, reinterpret_cast<uint32_t*>(x[1]));
-              kp_scores_ready(r);
-              kp_weights(x[1], r, w + 16 * c, masked, KP_HALF * h + 32 * c, lo, sk);
+              for (int q = 0; q < 32; ++q) v[q] *= down;
+              tmem_st32(O + c, reinterpret_cast<uint32_t (&)[32]>(v));
             }
           }
-          tmem_st32(S + KP_HALF / 2 * h, w);                           // over scores that have been read
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(&p_full[g][h]);
-          float s0, s1;
-          unpack_f2(add_f2(r.sum[0], r.sum[1]), s0, s1);
-          l += (s0 + s1) * scale;
         }
+        tmem_st32(S, *reinterpret_cast<uint32_t (*)[32]>(w));          // over scores that have been read
+        tmem_st32(S + 32, *reinterpret_cast<uint32_t (*)[32]>(w + 32));
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&p_full[g]);
+        l += sum * pow2i(-(int)F);
         ++used;
       }
       // ---- the output, divided by the sum ----
@@ -523,55 +526,47 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, int head0, int heads_here, 
         constexpr uint32_t ID_S = idesc_f16(128, KP_KT, false, false), ID_O = idesc_f16(128, D, false, true);
         bool ok = kp_wait(&q_full, 0, DEV_ERR_TIMEOUT_A);
         const uint32_t qd = desc_lo(smem_u32(sm + M::Q)), kd = desc_lo(smem_u32(sm + M::K)), vd = desc_lo(smem_u32(sm + M::V));
-        int used0 = 0, used1 = 0;                    // tiles used, by stream
+        int used0 = 0, used1 = 0;                    // tiles whose weights were used, by stream
         bool was0 = false, was1 = false;             // the last tile was one of the stream's
         for (int i = 0; i <= tiles.count && ok; ++i) {
           const bool more = i < tiles.count;
           const int j0 = more ? tiles.at(i) * KP_KT : 0;
+          const bool now0 = more && rows0.any(j0, KP_KT, a.window, a.sinks);
+          const bool now1 = more && rows1.any(j0, KP_KT, a.window, a.sinks);
           const uint32_t kb = kd + (i & 1) * (M::TILE >> 4), vb = vd + ((i - 1) & 1) * (M::TILE >> 4);
-          if (i > 0) ok = kp_wait(&v_full[(i - 1) & 1], ((i - 1) >> 1) & 1, DEV_ERR_TIMEOUT_FULL);
+          // every wait costs some 200 cycles here, also for what is long there: the copies' ones first,
+          // while the weights are still being computed
+          if (more) ok = kp_wait(&k_full[i & 1], (i >> 1) & 1, DEV_ERR_TIMEOUT_FULL);
+          if (i > 0 && ok) ok = kp_wait(&v_full[(i - 1) & 1], ((i - 1) >> 1) & 1, DEV_ERR_TIMEOUT_FULL);
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             int& used = g == 0 ? used0 : used1;
-            bool& was = g == 0 ? was0 : was1;
-            if (was) {
+            const bool was = g == 0 ? was0 : was1, now = g == 0 ? now0 : now1;
+            if (was && ok) ok = kp_wait(&p_full[g], used & 1, DEV_ERR_TIMEOUT_ACC);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              if (was) {
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                if (ok) ok = kp_wait(&p_full[g][h], used & 1, DEV_ERR_TIMEOUT_ACC);
-                if (ok) {
-                  tc_fence_after();
-                  if (elect_one()) {
-#pragma unroll
-                    for (int k = 0; k < KP_HALF / 16; ++k)
-                      mma_f16_ts(tmem + O_COL + 128u * g, tmem + S_COL + 128u * g + KP_HALF / 2 * h + 8 * k,
-                                 vb + h * (KP_HALF * 128 >> 4) + (2048 >> 4) * k, ID_O, h > 0 || k > 0 ? 1u : (uint32_t)used);
-                    if (h == 0) mma_commit(&o_done[g]);
-                  }
-                  __syncwarp();
-                }
+                for (int k = 0; k < KP_KT / 16; ++k)
+                  mma_f16_ts(tmem + O_COL + 128u * g, tmem + S_COL + 128u * g + 8 * k, vb + (2048 >> 4) * k, ID_O,
+                             k > 0 ? 1u : (uint32_t)used);
               }
-              ++used;
-            }
-            was = more && (g == 0 ? rows0 : rows1).any(j0, KP_KT, a.window, a.sinks);
-            // (a stream's wait also covers a tile that only the other stream sees)
-            if (more && ok) ok = kp_wait(&k_full[i & 1], (i >> 1) & 1, DEV_ERR_TIMEOUT_FULL);
-            if (was && ok) {
-              if (elect_one()) {
+              if (now) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                  mma_f16_ss(tmem + S_COL + 128u * g, qd + g * (M::TILE >> 4) + ((k >> 2) * 16384 + (k & 3) * 32 >> 4),
-                             kb + ((k >> 2) * 16384 + (k & 3) * 32 >> 4), ID_S, k > 0);
+                  mma_f16_ss(tmem + S_COL + 128u * g, qd + g * (M::TILE >> 4) + (((k >> 2) * 16384 + (k & 3) * 32) >> 4),
+                             kb + (((k >> 2) * 16384 + (k & 3) * 32) >> 4), ID_S, k > 0);
                 mma_commit(&s_full[g]);
               }
-              __syncwarp();
+              if (g == 1 && i > 0) mma_commit(&v_empty[(i - 1) & 1]);
+              if (g == 1 && more) mma_commit(&k_empty[i & 1]);
             }
+            __syncwarp();
+            if (was) ++used;
           }
-          if (!ok) break;
-          if (elect_one()) {
-            if (i > 0) mma_commit(&v_empty[(i - 1) & 1]);
-            if (more) mma_commit(&k_empty[i & 1]);
-          }
-          __syncwarp();
+          was0 = now0;
+          was1 = now1;
         }
         // completion of everything issued, also after a wait that gave up
         if (elect_one()) mma_commit(&all_done);
