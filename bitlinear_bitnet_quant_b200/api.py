@@ -387,84 +387,73 @@ def bitnet_kv4_cache(B: int, T_cap: int, kv_heads: int, head_dim: int = 128, dev
     return KV4Cache(codes(), steps(), codes(), steps())
 
 
-def _expect(t: torch.Tensor, name: str, dtype, shape, device):
-    """t is a contiguous tensor of this type and shape on this CUDA device."""
-    if not (t.is_cuda and t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous CUDA tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+def _expect(t: torch.Tensor, name: str, dtype, shape: tuple, device) -> int:
+    """The address of t, a contiguous tensor of this type and shape on this CUDA device."""
+    if t.device != device or t.dtype != dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+        if not (t.is_cuda and t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous CUDA tensor")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    return t.data_ptr()
 
 
 def _row_stride(t: torch.Tensor, name: str, rows: int, width: int, like: torch.Tensor) -> int:
     """Row stride, in values, of t [rows, width] with contiguous rows (a view of a wider tensor is fine)."""
-    if not (t.is_cuda and t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1)):
-        raise ValueError(f"{name} must be a CUDA tensor of contiguous rows")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
-    if t.dtype != like.dtype:
-        raise TypeError(f"{name} must be {like.dtype}, not {t.dtype}")
-    if t.shape[0] != rows or t.shape[1] != width:
-        raise ValueError(f"{name} must have shape {(rows, width)}, not {tuple(t.shape)}")
+    if t.shape != (rows, width) or t.stride(1) != 1 or t.dtype != like.dtype or t.device != like.device or not t.is_cuda:
+        if not (t.is_cuda and t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1)):
+            raise ValueError(f"{name} must be a CUDA tensor of contiguous rows")
+        if t.device != like.device:
+            raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+        if t.dtype != like.dtype:
+            raise TypeError(f"{name} must be {like.dtype}, not {t.dtype}")
+        if t.shape != (rows, width):
+            raise ValueError(f"{name} must have shape {(rows, width)}, not {tuple(t.shape)}")
     return t.stride(0) if rows > 1 else width
 
 
-def _step_args(pos, lens, B: int, device):
-    for t, n in ((pos, "pos"), (lens, "lens")):
-        if t is not None:
-            _expect(t, n, torch.int32, (B,), device)
-    return _ptr(pos), _ptr(lens)
+def _optional(t, name: str, dtype, shape: tuple, device):
+    return None if t is None else _expect(t, name, dtype, shape, device)
 
 
-def _cache_dims(cache: KV4Cache, B: int, device):
-    """(kv_heads, T_cap, d) of a 4-bit cache, checked."""
-    if cache.kc.dim() != 4:
+def _cache_args(cache: KV4Cache, B: int, device):
+    """(kv_heads, T_cap, d, the four addresses) of a 4-bit cache, checked."""
+    kc, ks, vc, vs = cache
+    if kc.dim() != 4:
         raise ValueError("a 4-bit cache's codes are [B, kv_heads, T_cap, d/2]")
-    _, kv, T, half = cache.kc.shape
-    for t, n in ((cache.kc, "cache.kc"), (cache.vc, "cache.vc")):
-        _expect(t, n, torch.uint8, (B, kv, T, half), device)
-    for t, n in ((cache.ks, "cache.ks"), (cache.vs, "cache.vs")):
-        _expect(t, n, torch.float32, (B, kv, T), device)
-    return kv, T, 2 * half
+    _, kv, T, half = kc.shape
+    codes, steps = (B, kv, T, half), (B, kv, T)
+    return kv, T, 2 * half, (_expect(kc, "cache.kc", torch.uint8, codes, device),
+                             _expect(ks, "cache.ks", torch.float32, steps, device),
+                             _expect(vc, "cache.vc", torch.uint8, codes, device),
+                             _expect(vs, "cache.vs", torch.float32, steps, device))
 
 
-class _On:
-    """Makes `device` current for the call; `stream` is the call's stream there."""
-
-    def __init__(self, device, stream):
-        self.stream = torch.cuda.current_stream(device) if stream is None else stream
-        self.ptr = ctypes.c_void_p(self.stream.cuda_stream)
-        self.guard = torch.cuda.device(device) if device.index != torch.cuda.current_device() else None
-        self.given = stream is not None
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-    def empty(self, shape, dtype, device):
-        """Memory that belongs to the call's stream."""
-        if not self.given:
-            return torch.empty(shape, dtype=dtype, device=device)
-        with torch.cuda.stream(self.stream):
-            return torch.empty(shape, dtype=dtype, device=device)
+def _empty(shape, dtype, device, stream, zero: bool = False) -> torch.Tensor:
+    """Memory that belongs to the call's stream, whichever stream and device are current."""
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
 
 
-def _append_rows(Q, K, V, B, L, heads, kv_heads, d, gamma_q, gamma_k):
-    rows, dev = B * L, Q.device
-    ld = (_row_stride(Q, "Q", rows, heads * d, Q), _row_stride(K, "K", rows, kv_heads * d, Q),
-          _row_stride(V, "V", rows, kv_heads * d, Q))
-    for t, n in ((gamma_q, "gamma_q"), (gamma_k, "gamma_k")):
-        if t is not None:
-            _expect(t, n, torch.float32, (d,), dev)
-    return ld
+def _call(fn: str, device, stream, args: tuple, allowed: int = 0) -> int:
+    """Enqueues fn(*args, stream) with `device` current; any status but 0 and `allowed` raises."""
+    raw = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    if device.index == torch._C._cuda_getDevice():
+        status = getattr(lib(), fn)(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            status = getattr(lib(), fn)(*args, raw)
+    if status != 0 and status != allowed:
+        raise BitnetError(fn, status)
+    return status
+
+
+_STATUS_WORKSPACE = 7
 
 
 def bitnet_qk_norm_rope_append(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, Kc: torch.Tensor, Vc: torch.Tensor,
@@ -477,22 +466,22 @@ def bitnet_qk_norm_rope_append(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor
     position t0 + pos[b] + l; only the first lens[b] tokens are real.  Returns the
     turned queries Qo, fp32 [B*L, heads*d] (pass Q itself, fp32, to turn in place)."""
     kv_heads = heads if kv_heads is None else kv_heads
-    dev = Q.device
+    dev, rows = Q.device, B * L
     _require(Kc, "Kc")
     T, d = Kc.shape[1], Kc.shape[2] // kv_heads
-    rot_dim = d if rot_dim is None else rot_dim
-    ldq, ldk, ldv = _append_rows(Q, K, V, B, L, heads, kv_heads, d, gamma_q, gamma_k)
-    for t, n in ((Kc, "Kc"), (Vc, "Vc")):
-        _expect(t, n, torch.float32, (B, T, kv_heads * d), dev)
-    p, ln = _step_args(pos, lens, B, dev)
-    with _On(dev, stream) as on:
-        if Qo is None:
-            Qo = on.empty((B * L, heads * d), torch.float32, dev)
-        _expect(Qo, "Qo", torch.float32, (B * L, heads * d), dev)
-        _check("bitnet_qk_norm_rope_append", lib().bitnet_qk_norm_rope_append(
-            _ptr(Q), _ptr(K), _ptr(V), _dtype_code(Q), ldq, ldk, ldv, B, L, t0, p, ln, heads, kv_heads, d,
-            _ptr(gamma_q), _ptr(gamma_k), float(eps), int(rot_dim), float(base), _ptr(Qo), _ptr(Kc), _ptr(Vc), T,
-            on.ptr))
+    ldq = _row_stride(Q, "Q", rows, heads * d, Q)
+    ldk = _row_stride(K, "K", rows, kv_heads * d, Q)
+    ldv = _row_stride(V, "V", rows, kv_heads * d, Q)
+    if Qo is None:
+        Qo = _empty((rows, heads * d), torch.float32, dev, stream)
+    _call("bitnet_qk_norm_rope_append", dev, stream, (
+        Q.data_ptr(), K.data_ptr(), V.data_ptr(), _dtype_code(Q), ldq, ldk, ldv, B, L, t0,
+        _optional(pos, "pos", torch.int32, (B,), dev), _optional(lens, "lens", torch.int32, (B,), dev), heads, kv_heads,
+        d, _optional(gamma_q, "gamma_q", torch.float32, (d,), dev),
+        _optional(gamma_k, "gamma_k", torch.float32, (d,), dev), eps, d if rot_dim is None else rot_dim, base,
+        _expect(Qo, "Qo", torch.float32, (rows, heads * d), dev),
+        _expect(Kc, "Kc", torch.float32, (B, T, kv_heads * d), dev),
+        _expect(Vc, "Vc", torch.float32, (B, T, kv_heads * d), dev), T))
     return Qo
 
 
@@ -504,22 +493,22 @@ def bitnet_kv4_append(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cache: 
     and the append of keys and values to a 4-bit cache.  Rows as for
     bitnet_qk_norm_rope_append.  Returns the turned queries Qo [B*L, heads*d], in Q's
     type unless passed in (fp32 or bf16; Q itself turns in place)."""
-    dev = Q.device
+    dev, rows = Q.device, B * L
     if not Q.is_cuda:
         raise ValueError("Q must be a CUDA tensor of contiguous rows")
-    kv, T, d = _cache_dims(cache, B, dev)
-    rot_dim = d if rot_dim is None else rot_dim
-    ldq, ldk, ldv = _append_rows(Q, K, V, B, L, heads, kv, d, gamma_q, gamma_k)
-    p, ln = _step_args(pos, lens, B, dev)
-    flags = (1 if norm else 0) | (2 if hadamard else 0)
-    with _On(dev, stream) as on:
-        if Qo is None:
-            Qo = on.empty((B * L, heads * d), Q.dtype, dev)
-        _expect(Qo, "Qo", Qo.dtype, (B * L, heads * d), dev)
-        _check("bitnet_kv4_append", lib().bitnet_kv4_append(
-            _ptr(Q), _ptr(K), _ptr(V), _dtype_code(Q), ldq, ldk, ldv, B, L, t0, p, ln, heads, kv, d, _ptr(gamma_q),
-            _ptr(gamma_k), float(eps), int(rot_dim), float(base), flags, _ptr(Qo), _dtype_code(Qo), _ptr(cache.kc),
-            _ptr(cache.ks), _ptr(cache.vc), _ptr(cache.vs), T, on.ptr))
+    kv, T, d, held = _cache_args(cache, B, dev)
+    ldq = _row_stride(Q, "Q", rows, heads * d, Q)
+    ldk = _row_stride(K, "K", rows, kv * d, Q)
+    ldv = _row_stride(V, "V", rows, kv * d, Q)
+    if Qo is None:
+        Qo = _empty((rows, heads * d), Q.dtype, dev, stream)
+    _call("bitnet_kv4_append", dev, stream, (
+        Q.data_ptr(), K.data_ptr(), V.data_ptr(), _dtype_code(Q), ldq, ldk, ldv, B, L, t0,
+        _optional(pos, "pos", torch.int32, (B,), dev), _optional(lens, "lens", torch.int32, (B,), dev), heads, kv, d,
+        _optional(gamma_q, "gamma_q", torch.float32, (d,), dev),
+        _optional(gamma_k, "gamma_k", torch.float32, (d,), dev), eps, d if rot_dim is None else rot_dim, base,
+        (1 if norm else 0) | (2 if hadamard else 0), _expect(Qo, "Qo", Qo.dtype, (rows, heads * d), dev),
+        _dtype_code(Qo), *held, T))
     return Qo
 
 
@@ -530,24 +519,14 @@ def bitnet_kv4_read(cache: KV4Cache, B: int, L: int, t0: int, pos=None, lens=Non
     padding and of positions outside the cache are left as they were (zeros where the
     tensors are allocated here)."""
     dev = cache.kc.device
-    kv, T, d = _cache_dims(cache, B, dev)
-    p, ln = _step_args(pos, lens, B, dev)
-    with _On(dev, stream) as on:
-        dtype = K.dtype if K is not None else V.dtype if V is not None else dtype
-        fresh = lambda: on.empty((B * L, kv * d), dtype, dev)
-        K_new, V_new = K is None, V is None
-        K, V = (fresh() if K_new else K), (fresh() if V_new else V)
-        for t, n in ((K, "K"), (V, "V")):
-            _expect(t, n, dtype, (B * L, kv * d), dev)
-        if (K_new or V_new) and (pos is not None or lens is not None):
-            with torch.cuda.stream(on.stream):
-                if K_new:
-                    K.zero_()
-                if V_new:
-                    V.zero_()
-        _check("bitnet_kv4_read", lib().bitnet_kv4_read(
-            _ptr(cache.kc), _ptr(cache.ks), _ptr(cache.vc), _ptr(cache.vs), B, L, t0, p, ln, kv, d, T, _ptr(K), _ptr(V),
-            _dtype_code(K), on.ptr))
+    kv, T, d, held = _cache_args(cache, B, dev)
+    dtype = K.dtype if K is not None else V.dtype if V is not None else dtype
+    shape, partial = (B * L, kv * d), pos is not None or lens is not None
+    K = _empty(shape, dtype, dev, stream, zero=partial) if K is None else K
+    V = _empty(shape, dtype, dev, stream, zero=partial) if V is None else V
+    _call("bitnet_kv4_read", dev, stream, (
+        *held, B, L, t0, _optional(pos, "pos", torch.int32, (B,), dev), _optional(lens, "lens", torch.int32, (B,), dev),
+        kv, d, T, _expect(K, "K", dtype, shape, dev), _expect(V, "V", dtype, shape, dev), _dtype_code(K)))
     return K, V
 
 
@@ -571,28 +550,23 @@ def bitnet_kv4_attention(Q: torch.Tensor, cache: KV4Cache, B: int, L: int, t0: i
     dev = Q.device
     if not Q.is_cuda:
         raise ValueError("Q must be a contiguous CUDA tensor")
-    kv, T, d = _cache_dims(cache, B, dev)
-    _expect(Q, "Q", Q.dtype, (B * L, heads * d), dev)
-    p, ln = _step_args(pos, lens, B, dev)
-    if t_max is None:
-        t_max = t0 + L if pos is None else T
-    with _On(dev, stream) as on:
-        if A is None:
-            A = on.empty((B * L, heads * d), Q.dtype, dev)
-            if lens is not None:
-                with torch.cuda.stream(on.stream):
-                    A.zero_()
-        _expect(A, "A", Q.dtype, (B * L, heads * d), dev)
-        t_max, code = min(int(t_max), T), _dtype_code(Q)
-        need = lib().bitnet_kv4_attention_workspace_size(code, B, L, heads, kv, d, T, int(window), int(sinks), t_max)
-        if workspace is None:
-            workspace = on.empty((need,), torch.uint8, dev) if need else None
-        else:
-            _expect(workspace, "workspace", torch.uint8, workspace.shape, dev)
-        _check("bitnet_kv4_attention", lib().bitnet_kv4_attention(
-            _ptr(Q), code, _ptr(cache.kc), _ptr(cache.ks), _ptr(cache.vc), _ptr(cache.vs), B, L, t0, p, ln,
-            heads, kv, d, T, int(window), int(sinks), t_max, _ptr(A), _ptr(workspace),
-            0 if workspace is None else workspace.numel(), on.ptr))
+    kv, T, d, held = _cache_args(cache, B, dev)
+    shape = (B * L, heads * d)
+    t_max = min(T, (t0 + L if pos is None else T) if t_max is None else t_max)
+    if A is None:
+        A = _empty(shape, Q.dtype, dev, stream, zero=lens is not None)
+    code = _dtype_code(Q)
+    args = (_expect(Q, "Q", Q.dtype, shape, dev), code, *held, B, L, t0,
+            _optional(pos, "pos", torch.int32, (B,), dev), _optional(lens, "lens", torch.int32, (B,), dev), heads, kv, d,
+            T, window, sinks, t_max, _expect(A, "A", Q.dtype, shape, dev))
+    if workspace is not None:
+        scratch = (_expect(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.numel())
+        _call("bitnet_kv4_attention", dev, stream, args + scratch)
+    elif _call("bitnet_kv4_attention", dev, stream, args + (None, 0), allowed=_STATUS_WORKSPACE):
+        # many queries: nothing was enqueued yet
+        need = bitnet_kv4_attention_workspace_size(Q.dtype, B, L, heads, kv, d, T, window, sinks, t_max)
+        workspace = _empty((need,), torch.uint8, dev, stream)
+        _call("bitnet_kv4_attention", dev, stream, args + (workspace.data_ptr(), need))
     return A
 
 
