@@ -25,6 +25,8 @@
 
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 namespace bitnet {
 
 constexpr int KVA_WARPS = 8;
@@ -75,6 +77,70 @@ BN_DEV void turn_pair(const float2 w, float& a, float& b) {
   b = x * w.y + y * w.x;
 }
 
+// Hadamard transform of a head's row, 8 values a lane: strides 1, 2, 4 in the lane, the
+// others across lanes (y = +-y + the partner's).
+template <int D>
+BN_DEV void hadamard_row(double (&y)[8], int q) {
+#pragma unroll
+  for (int st = 1; st < 8; st <<= 1) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if ((i & st) == 0) {
+        const double a = y[i], b = y[i + st];
+        y[i] = a + b;
+        y[i + st] = a - b;
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 1; o < D / 8; o <<= 1) {
+    const double sign = (q & o) ? -1.0 : 1.0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = y[i] * sign + __shfl_xor_sync(0xffffffffu, y[i], o);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] *= D == 128 ? 0.08838834764831844055 : 0.125;      // 1 / sqrt(d)
+}
+// In fp32 on pairs: half the instructions.
+template <int D>
+BN_DEV void hadamard_row(float (&y)[8], int q) {
+  uint64_t v[4];
+  const uint64_t neg = pack_f2(-1.f, -1.f), alt = pack_f2(1.f, -1.f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)                        // stride 1: (a + b, a - b)
+    v[i] = fma_f2(pack_f2(y[2 * i + 1], y[2 * i + 1]), alt, pack_f2(y[2 * i], y[2 * i]));
+#pragma unroll
+  for (int st = 1; st < 4; st <<= 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if ((i & st) == 0) {
+        const uint64_t a = v[i], b = v[i + st];
+        v[i] = add_f2(a, b);
+        v[i + st] = fma_f2(b, neg, a);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 1; o < D / 8; o <<= 1) {
+    const float sign = (q & o) ? -1.f : 1.f;
+    const uint64_t sign2 = pack_f2(sign, sign);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float a, b;
+      unpack_f2(v[i], a, b);
+      v[i] = fma_f2(v[i], sign2, pack_f2(__shfl_xor_sync(0xffffffffu, a, o), __shfl_xor_sync(0xffffffffu, b, o)));
+    }
+  }
+  const float f = D == 128 ? 0.08838834764831844055f : 0.125f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    unpack_f2(v[i], a, b);
+    y[2 * i] = a * f;
+    y[2 * i + 1] = b * f;
+  }
+}
+
 // Norm, rotation and Hadamard of a head's row, in CT arithmetic: 8 values of the row a
 // lane, dimensions 8 q .. 8 q + 7 for lane q of the head's LPH lanes.
 template <typename CT, typename CS, int D>
@@ -104,33 +170,16 @@ BN_DEV void turn_row(const float (&x)[8], float (&t)[8], int q, int norm, const 
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (8 * q + 2 * i < rot_dim) turn_pair(cs[i * LPH + q], y[2 * i], y[2 * i + 1]);
-  if (hadamard) {
-#pragma unroll
-    for (int st = 1; st < 8; st <<= 1) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if ((i & st) == 0) {
-          const CT a = y[i], b = y[i + st];
-          y[i] = a + b;
-          y[i + st] = a - b;
-        }
-      }
-    }
-#pragma unroll
-    for (int o = 1; o < LPH; o <<= 1) {
-      const CT sign = (q & o) ? (CT)-1 : (CT)1;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = y[i] * sign + __shfl_xor_sync(0xffffffffu, y[i], o);
-    }
-    const CT f = (CT)(D == 128 ? 0.08838834764831844055 : 0.125);    // 1 / sqrt(d)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] *= f;
-  }
+  if (hadamard) hadamard_row<D>(y, q);
 #pragma unroll
   for (int i = 0; i < 8; ++i) t[i] = (float)y[i];
 }
 
 // A lane's 8 values of a row to a word of codes; every lane of the row gets the step.
+// rint(t s) + 8 stands in the low bits of t s + (1.5 * 2^23 + 8), rounded to nearest even;
+// the shifted sum of eight such words, less that of their constant parts (modulo 2^32),
+// is the word of biased codes.  |t s| <= 7 up to its rounding, so that no code needs the
+// clamp to -8 .. 7.
 template <int D>
 BN_DEV uint32_t row_to_codes(const float (&t)[8], float& step) {
   constexpr int LPH = D / 8;
@@ -141,21 +190,21 @@ BN_DEV uint32_t row_to_codes(const float (&t)[8], float& step) {
   for (int o = 1; o < LPH; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   const float s = __fdiv_rn(7.0f, fmaxf(mx, 1e-5f));
   step = __fdiv_rn(1.0f, s);
-  uint32_t w = 0u;
+  uint32_t w = 0u, constant = 0u;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    int c = __float2int_rn(__fmul_rn(t[i], s));
-    c = c < -8 ? -8 : (c > 7 ? 7 : c);
-    w |= (uint32_t)(c & 15) << (4 * (i >> 1) + 16 * (i & 1));
+    const int at = 4 * (i >> 1) + 16 * (i & 1);
+    w += __float_as_uint(__fadd_rn(__fmul_rn(t[i], s), 12582920.f)) << at;
+    constant += 0x4B400000u << at;
   }
-  return w;
+  return (w - constant) ^ 0x88888888u;
 }
 
 // Grid: x over groups of `tokens` rows of the step.  A unit is one warp's heads of K, V
 // or Q of one token.  tokens == KVA_WARPS: a warp takes every unit of its token;
 // tokens == 1: the token's units over the warps of the y blocks, one each.
 template <int D, typename XT, bool FOUR>
-__global__ void __launch_bounds__(32 * KVA_WARPS)
+__global__ void __launch_bounds__(32 * KVA_WARPS, 4)
 append_kernel(const KvStep s, const AppendArgs a, const __grid_constant__ RopeTable rope, int tokens) {
   constexpr int LPH = D / 8, HPW = 32 / LPH, PAIRS = D / 2;
   extern __shared__ double2 cs64[];                  // [tokens][PAIRS] cosine, sine; then the same in fp32
@@ -187,54 +236,79 @@ append_kernel(const KvStep s, const AppendArgs a, const __grid_constant__ RopeTa
   const bool in = p >= 0 && p < s.T_cap;             // a row outside the cache is not appended
   const int q = lane % LPH, hw = lane / LPH;
   const int uk = (a.kv_heads + HPW - 1) / HPW, uq = (a.heads + HPW - 1) / HPW;
-  const int units = 2 * uk + uq, stride = tokens == 1 ? units : 1;
-  int u = tokens == 1 ? (int)blockIdx.y * KVA_WARPS + warp : 0;
-  auto head_of = [&](int v) { return (v < uk ? v : v < 2 * uk ? v - uk : v - 2 * uk) * HPW + hw; };
-  auto load = [&](int v, Raw8<XT>& r) {              // K units, then V, then Q
-    const int kind = v < uk ? 0 : (v < 2 * uk ? 1 : 2), h = head_of(v);
+  const double2* c64 = cs64 + tk * PAIRS;
+  const float2* c32 = cs32 + tk * PAIRS;
+
+  // `count` units of one kind (0 keys, 1 values, 2 queries) from head h0 on, the next unit's rows
+  // loaded while one is worked on
+  auto units = [&](auto kind_c, const void* base, int64_t ld, int n_heads, int h0, int count) {
+    constexpr int KIND = decltype(kind_c)::value;
+    int h = h0 + hw;
+    const XT* src = static_cast<const XT*>(base) + (int64_t)row * ld + h * D + 8 * q;
+    auto load = [&](bool real, Raw8<XT>& r) {
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(XT) / 2; ++i) r.v[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (v < units && h < (kind == 2 ? a.heads : a.kv_heads)) {
-      const XT* src = static_cast<const XT*>(kind == 0 ? a.K : kind == 1 ? a.V : a.Q);
-      load8<XT>(src + (int64_t)row * (kind == 0 ? a.ldk : kind == 1 ? a.ldv : a.ldq) + h * D + 8 * q, r);
+      for (int i = 0; i < (int)sizeof(XT) / 2; ++i) r.v[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (real) load8<XT>(src, r);
+      src += HPW * D;
+    };
+    Raw8<XT> next;
+    load(h < n_heads, next);
+    // where a row goes: Qo, or the caches at the token's position
+    int64_t at = KIND == 2 ? ((int64_t)row * a.heads + h) * D + 8 * q
+                 : FOUR    ? ((int64_t)b * a.kv_heads + h) * s.T_cap + p
+                           : (((int64_t)b * s.T_cap + p) * a.kv_heads + h) * D + 8 * q;
+    const int64_t step_at = KIND != 2 && FOUR ? (int64_t)HPW * s.T_cap : HPW * D;
+    for (int v = 0; v < count; ++v, h += HPW, at += step_at) {
+      float x[8], t[8];
+      values8(next, x);
+      if (v + 1 < count) load(h + HPW < n_heads, next);
+      const bool real = h < n_heads;
+      if constexpr (KIND == 2) {
+        turn_row<float, float2, D>(x, t, q, a.norm, a.gamma_q, a.eps, a.rot_dim, c32, a.hadamard);
+        if (real) {
+          if (a.qo_bf16) store8_bf16(static_cast<__nv_bfloat16*>(a.Qo) + at, t);
+          else store8_f32(static_cast<float*>(a.Qo) + at, t);
+        }
+      } else {
+        if constexpr (KIND == 1) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) t[i] = x[i];
+        } else if constexpr (FOUR) {
+          turn_row<double, double2, D>(x, t, q, a.norm, a.gamma_k, a.eps, a.rot_dim, c64, a.hadamard);
+        } else {
+          turn_row<float, float2, D>(x, t, q, a.norm, a.gamma_k, a.eps, a.rot_dim, c32, 0);
+        }
+        if constexpr (FOUR) {
+          float step;
+          const uint32_t w = row_to_codes<D>(t, step);
+          if (real && in) {
+            *reinterpret_cast<uint32_t*>((KIND == 0 ? a.Kc4 : a.Vc4) + at * (D / 2) + 4 * q) = w;
+            if (q == 0) (KIND == 0 ? a.Ks : a.Vs)[at] = step;
+          }
+        } else if (real && in) {
+          store8_f32((KIND == 0 ? a.Kc32 : a.Vc32) + at, t);
+        }
+      }
     }
   };
-  Raw8<XT> next;
-  load(u, next);
-  for (; u < units; u += stride) {
-    float x[8], t[8];
-    values8(next, x);
-    if (stride == 1) load(u + 1, next);              // the next unit's rows meanwhile
-    const int kind = u < uk ? 0 : (u < 2 * uk ? 1 : 2), h = head_of(u);
-    const bool real = h < (kind == 2 ? a.heads : a.kv_heads);
-    if (kind == 2) {
-      turn_row<float, float2, D>(x, t, q, a.norm, a.gamma_q, a.eps, a.rot_dim, cs32 + tk * PAIRS, a.hadamard);
-      if (real) {
-        const int64_t off = (int64_t)row * a.heads * D + h * D + 8 * q;
-        if (a.qo_bf16) store8_bf16(static_cast<__nv_bfloat16*>(a.Qo) + off, t);
-        else store8_f32(static_cast<float*>(a.Qo) + off, t);
-      }
-      continue;
-    }
-    if (kind == 0) {
-      if (FOUR) turn_row<double, double2, D>(x, t, q, a.norm, a.gamma_k, a.eps, a.rot_dim, cs64 + tk * PAIRS, a.hadamard);
-      else turn_row<float, float2, D>(x, t, q, a.norm, a.gamma_k, a.eps, a.rot_dim, cs32 + tk * PAIRS, 0);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] = x[i];
-    }
-    if (FOUR) {
-      float step;
-      const uint32_t w = row_to_codes<D>(t, step);
-      if (real && in) {
-        const int64_t cr = ((int64_t)b * a.kv_heads + h) * s.T_cap + p;
-        *reinterpret_cast<uint32_t*>((kind == 0 ? a.Kc4 : a.Vc4) + cr * (D / 2) + 4 * q) = w;
-        if (q == 0) (kind == 0 ? a.Ks : a.Vs)[cr] = step;
-      }
-    } else if (real && in) {
-      store8_f32((kind == 0 ? a.Kc32 : a.Vc32) + (((int64_t)b * s.T_cap + p) * a.kv_heads + h) * D + 8 * q, t);
-    }
+  using Keys = std::integral_constant<int, 0>;
+  using Values = std::integral_constant<int, 1>;
+  using Queries = std::integral_constant<int, 2>;
+  int first = 0, count = 0x7fffffff;                 // this warp's units among K, V, Q in turn
+  if (tokens == 1) {
+    first = (int)blockIdx.y * KVA_WARPS + warp;
+    count = 1;
   }
+  auto part = [&](int lo, int n, int& f, int& k) {   // of units lo .. lo + n - 1
+    f = first > lo ? first - lo : 0;
+    const int64_t end = (int64_t)first + count - lo;
+    k = (int)(end < n ? end : n) - f;
+    return k > 0;
+  };
+  int f, k;
+  if (part(0, uk, f, k)) units(Keys(), a.K, a.ldk, a.kv_heads, f * HPW, k);
+  if (part(uk, uk, f, k)) units(Values(), a.V, a.ldv, a.kv_heads, f * HPW, k);
+  if (part(2 * uk, uq, f, k)) units(Queries(), a.Q, a.ldq, a.heads, f * HPW, k);
 }
 
 // ---------------------------------------------------------------------------

@@ -56,28 +56,31 @@ BN_DEV float ld_cluster_f32(uint32_t addr) {
   return v;
 }
 
-// A tile's codes and steps into one stage.  Keys past the cache's end are zero.
-// Value rows 2t of each 8 lie first, then rows 2t + 1: the product's lanes read rows
-// 2t (t = 0..3) at once, then without bank conflicts.
+// A tile's codes and steps into one stage: a tile is one run of memory, lane i copies
+// every 32nd 16 bytes.  Keys past the cache's end are zero.  Value rows 2t of each 8 lie
+// first, then rows 2t + 1: the product's lanes read rows 2t (t = 0..3) at once, then
+// without bank conflicts.
 template <int D>
 BN_DEV void kd_stage(const uint8_t* kc, const float* ks, const uint8_t* vc, const float* vs, int j0, int T_cap,
-                     uint8_t* stage, int lane) {
+                     uint32_t dst, int lane) {
   constexpr int CPR = D / 32;                        // 16-byte chunks a row
-  const uint32_t dst = smem_u32(stage);
+  const uint8_t* k = kc + (int64_t)j0 * (D / 2) + 16 * lane;
+  const uint8_t* v = vc + (int64_t)j0 * (D / 2) + 16 * lane;
+  const bool whole = j0 + KD_KT <= T_cap;
 #pragma unroll
   for (int i = 0; i < CPR; ++i) {
-    const int e = lane + 32 * i, r = e / CPR, c = e - r * CPR;
-    const bool in = j0 + r < T_cap;
-    const int64_t off = in ? (int64_t)(j0 + r) * (D / 2) + 16 * c : 0;
+    const int r = (lane + 32 * i) / CPR, c = (lane + 32 * i) % CPR;
     const int vr = (r & ~7) | ((r & 7) >> 1) | ((r & 1) << 2);
-    cp_async_16(dst + r * (D / 2) + 16 * c, kc + off, in ? 16u : 0u);
-    cp_async_16(dst + KdTile<D>::CODES + vr * (D / 2) + 16 * c, vc + off, in ? 16u : 0u);
+    const bool in = whole || j0 + r < T_cap;
+    cp_async_16(dst + 16 * (lane + 32 * i), in ? k + 512 * i : kc, in ? 16u : 0u);
+    cp_async_16(dst + KdTile<D>::CODES + vr * (D / 2) + 16 * c, in ? v + 512 * i : vc, in ? 16u : 0u);
   }
   if (lane < 16) {
     const int c = lane & 7;                          // 4 steps a chunk (T_cap is a multiple of 16)
-    const bool in = j0 + 4 * c < T_cap;
-    const float* src = (lane < 8 ? ks : vs) + (in ? j0 + 4 * c : 0);
-    cp_async_16(dst + 2 * KdTile<D>::CODES + (lane < 8 ? 0 : KD_KT * 4) + 16 * c, src, in ? 16u : 0u);
+    const bool in = whole || j0 + 4 * c < T_cap;
+    const float* src = lane < 8 ? ks : vs;
+    cp_async_16(dst + 2 * KdTile<D>::CODES + (lane < 8 ? 0 : KD_KT * 4) + 16 * c, in ? src + j0 + 4 * c : src,
+                in ? 16u : 0u);
   }
 }
 
@@ -177,6 +180,7 @@ kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e) {
   const float* ks = a.Ks + head * s.T_cap;
   const float* vs = a.Vs + head * s.T_cap;
   uint8_t* ring = kd_smem + warp * KD_STAGES * KdTile<D>::BYTES;
+  const uint32_t ring_a = smem_u32(ring);
 
   float m[NT][2], l[NT][2], o[NT][MT][4];
 #pragma unroll
@@ -193,7 +197,7 @@ kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e) {
 #pragma unroll
   for (int i = 0; i < KD_STAGES - 1; ++i) {
     if (i < mine)
-      kd_stage<D>(kc, ks, vc, vs, tiles.at(first + i * stride) * KD_KT, s.T_cap, ring + i * KdTile<D>::BYTES, lane);
+      kd_stage<D>(kc, ks, vc, vs, tiles.at(first + i * stride) * KD_KT, s.T_cap, ring_a + i * KdTile<D>::BYTES, lane);
     cp_async_commit();
   }
   for (int it = 0; it < mine; ++it) {
@@ -203,7 +207,7 @@ kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e) {
       const int nx = it + KD_STAGES - 1;
       if (nx < mine)
         kd_stage<D>(kc, ks, vc, vs, tiles.at(first + nx * stride) * KD_KT, s.T_cap,
-                    ring + (nx % KD_STAGES) * KdTile<D>::BYTES, lane);
+                    ring_a + (nx % KD_STAGES) * KdTile<D>::BYTES, lane);
       cp_async_commit();
     }
     const uint8_t* stage = ring + (it % KD_STAGES) * KdTile<D>::BYTES;
@@ -211,13 +215,18 @@ kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e) {
     const float* vst = kst + KD_KT;
     const int j0 = tiles.at(first + it * stride) * KD_KT;
     // ---- scores of keys 16 x + g, + 8 (rows) and queries 2t, 2t + 1 (columns) ----
-    float sc[2][NT][4];
+    // (fp32: the products of the second terms are summed apart, so that the first ones' sum is cut
+    // off half as often)
+    float sc[2][NT][4], sl[SPLIT ? 2 : 1][SPLIT ? NT : 1][4];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) sc[x][n][c] = 0.f;
+        for (int c = 0; c < 4; ++c) {
+          sc[x][n][c] = 0.f;
+          if constexpr (SPLIT) sl[x][n][c] = 0.f;
+        }
       const uint8_t* kr = stage + (16 * x + g) * (D / 2) + 4 * KW * t;
       uint32_t w0[KW], w1[KW];
       if constexpr (KW == 4) {
@@ -241,7 +250,7 @@ kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e) {
             mma_f16(sc[x][n], k0[2 * u], k1[2 * u], k0[2 * u + 1], k1[2 * u + 1], qh[n][4 * i + 2 * u],
                     qh[n][4 * i + 2 * u + 1]);
             if constexpr (SPLIT)
-              mma_f16(sc[x][n], k0[2 * u], k1[2 * u], k0[2 * u + 1], k1[2 * u + 1], ql[n][4 * i + 2 * u],
+              mma_f16(sl[x][n], k0[2 * u], k1[2 * u], k0[2 * u + 1], k1[2 * u + 1], ql[n][4 * i + 2 * u],
                       ql[n][4 * i + 2 * u + 1]);
           }
         }
@@ -252,23 +261,39 @@ kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e) {
     const bool full = rows_in && j0 + KD_KT - 1 <= p_lo &&
                       (a.window == 0 || j0 > p_hi - a.window || j0 + KD_KT <= a.sinks);
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
+    for (int x = 0; x < 2; ++x)
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int key = 16 * x + 8 * y + g;
         const float kstep = kst[key], vstep = vst[key];
-        const int e = step_exponent(vstep);
-        inv[x][y] = pow2i(-e);
+        // the exponent field, clamped as in step_exponent; as a float through the low bits of 2^23
+        int e = (int)(__float_as_uint(vstep) >> 23);
+        e = e < 103 ? 103 : (e > 253 ? 253 : e);
+        const float ef = __uint_as_float(0x4B000000u + (uint32_t)e) - 8388735.f;
+        inv[x][y] = __uint_as_float((uint32_t)(254 - e) << 23);
         f[x][y] = vstep * inv[x][y];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float v = sc[x][n][2 * y + i] * (kstep * unscale[n][i]) + (float)e;
-            sc[x][n][2 * y + i] = full || key_visible(j0 + key, pos[n][i], a.window, a.sinks) ? v : -INFINITY;
+            float acc = sc[x][n][2 * y + i];
+            if constexpr (SPLIT) acc += sl[x][n][2 * y + i];
+            sc[x][n][2 * y + i] = acc * (kstep * unscale[n][i]) + ef;
           }
+        if (!full) {
+          // masked scores; a value step that is not finite is NaN to the queries that see the key, through
+          // the score, and zero in the operand
+          const bool finite = fabsf(vstep) < INFINITY;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float& v = sc[x][n][2 * y + i];
+              v = !key_visible(j0 + key, pos[n][i], a.window, a.sinks) ? -INFINITY : finite ? v : NAN;
+            }
+          if (!finite) f[x][y] = 0.f;
+        }
       }
-    }
     // ---- running maximum (a query's keys lie in the 8 lanes of one t), weights, sums ----
     bool moved = false;
     float corr[NT][2];
@@ -295,7 +320,7 @@ kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e) {
           for (int q = 0; q < MT; ++q) { o[n][q][i] *= corr[n][i]; o[n][q][2 + i] *= corr[n][i]; }
         }
     }
-    uint32_t ph[2][NT][2], pr[2][NT][2];
+    uint32_t ph[2][NT][2], pr[SPLIT ? 2 : 1][SPLIT ? NT : 1][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const float ref0 = m[n][0] == -INFINITY ? 0.f : m[n][0] - BIAS;
@@ -305,11 +330,9 @@ kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e) {
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           const float e0 = ex2(sc[x][n][2 * y] - ref0), e1 = ex2(sc[x][n][2 * y + 1] - ref1);
-          // a masked key's weight is zero whatever its steps hold
-          const bool s0 = sc[x][n][2 * y] != -INFINITY, s1 = sc[x][n][2 * y + 1] != -INFINITY;
-          l[n][0] += s0 ? e0 * inv[x][y] : 0.f;
-          l[n][1] += s1 ? e1 * inv[x][y] : 0.f;
-          const float w0 = s0 ? e0 * f[x][y] : 0.f, w1 = s1 ? e1 * f[x][y] : 0.f;
+          l[n][0] += e0 * inv[x][y];
+          l[n][1] += e1 * inv[x][y];
+          const float w0 = e0 * f[x][y], w1 = e1 * f[x][y];
           const uint32_t hi = pack_half2(w0, w1);
           ph[x][n][y] = transpose8x8(hi);
           if constexpr (SPLIT) pr[x][n][y] = transpose8x8(half2_rest(hi, w0, w1));
@@ -340,8 +363,17 @@ kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e) {
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            mma_f16(o[n][4 * i + j], a0[j], a1[j], a2[j], a3[j], ph[x][n][0], ph[x][n][1]);
-            if constexpr (SPLIT) mma_f16(o[n][4 * i + j], a0[j], a1[j], a2[j], a3[j], pr[x][n][0], pr[x][n][1]);
+            if constexpr (SPLIT) {
+              // the tensor cores cut their sums off: 16 keys' products are summed there, the output with
+              // rounding here
+              float part[4] = {0.f, 0.f, 0.f, 0.f};
+              mma_f16(part, a0[j], a1[j], a2[j], a3[j], pr[x][n][0], pr[x][n][1]);
+              mma_f16(part, a0[j], a1[j], a2[j], a3[j], ph[x][n][0], ph[x][n][1]);
+#pragma unroll
+              for (int c = 0; c < 4; ++c) o[n][4 * i + j][c] += part[c];
+            } else {
+              mma_f16(o[n][4 * i + j], a0[j], a1[j], a2[j], a3[j], ph[x][n][0], ph[x][n][1]);
+            }
           }
       }
     }
@@ -433,13 +465,16 @@ static cudaError_t launch_decode(const KvStep& s, const AttnArgs& a, int64_t t_m
   const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   const int64_t row_tiles = ((int64_t)s.L * (a.heads / a.kv_heads) + ROWS - 1) / ROWS;
-  // a cluster splits the keys of one row tile: as long as the blocks fit the GPU two
-  // or three to an SM and every warp has a few tiles
+  // a cluster splits the keys of one row tile: until the blocks fill the GPU (three to an
+  // SM) with two tiles a warp at least, and, as sequences may be of very different lengths,
+  // until no warp has more than 16 tiles.  (16 sequences of 2048 to 32768 keys, 8 key heads:
+  // two blocks a cluster 179 us, eight XXX us.)
   const int64_t blocks = row_tiles * a.kv_heads * s.B;
   int64_t keys = t_max;
   if (a.window > 0 && (int64_t)a.window + a.sinks + s.L < keys) keys = (int64_t)a.window + a.sinks + s.L;
+  const int64_t per_tile = KD_WARPS * KD_KT;         // keys a block takes with one tile a warp
   unsigned c = 1;
-  while (c < 8 && blocks * c * 2 <= 3 * 148 && keys > (int64_t)c * KD_WARPS * KD_KT * 2) c *= 2;
+  while (c < 8 && ((blocks * c * 2 <= 3 * 148 && keys > c * per_tile * 2) || keys > c * per_tile * 16)) c *= 2;
   return launch_pdl(kern, dim3((unsigned)(row_tiles * c), (unsigned)a.kv_heads, (unsigned)s.B), dim3(32 * KD_WARPS),
                     smem, st, dim3(c, 1, 1), s, a, (float)(1.4426950408889634 / sqrt((double)D)));
 }

@@ -98,6 +98,29 @@ BN_DEV uint32_t half2_rest(uint32_t h, float lo, float hi) {
   return pack_half2(lo - f.x, hi - f.y);
 }
 
+// Pairs of fp32 in one register pair, and operations on both at once.
+BN_DEV uint64_t pack_f2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+BN_DEV void unpack_f2(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+BN_DEV uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+BN_DEV uint64_t add_f2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+BN_DEV float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // A step's exponent e, at least -24: the append writes steps of 2^-20 and more (or a
 // row is empty, step 0, and keeps its weight in the sum).  Together with steps below
 // 2^60 no weight p' that counts leaves the range of fp32 (2^-126): 2^(-24 - 60) of
