@@ -31,7 +31,7 @@ namespace bitnet {
 // memory, the blocks of a cluster over distributed shared memory.
 // ---------------------------------------------------------------------------
 constexpr int KD_WARPS = 4;
-constexpr int KD_STAGES = 4;
+constexpr int KD_STAGES = 3;
 constexpr int KD_KT = 32;                            // keys a tile
 
 template <int D>
@@ -64,28 +64,32 @@ template <int D>
 BN_DEV void kd_stage(const uint8_t* kc, const float* ks, const uint8_t* vc, const float* vs, int j0, int T_cap,
                      uint32_t dst, int lane) {
   constexpr int CPR = D / 32;                        // 16-byte chunks a row
-  const uint8_t* k = kc + (int64_t)j0 * (D / 2) + 16 * lane;
-  const uint8_t* v = vc + (int64_t)j0 * (D / 2) + 16 * lane;
-  const bool whole = j0 + KD_KT <= T_cap;
+  const int64_t off = (int64_t)j0 * (D / 2) + 16 * lane;
+  const int c = lane & 7;                            // 4 steps a chunk (T_cap is a multiple of 16)
+  const float* steps = (lane < 8 ? ks : vs) + j0 + 4 * c;
+  const uint32_t steps_dst = dst + 2 * KdTile<D>::CODES + (lane < 8 ? 0 : KD_KT * 4) + 16 * c;
 #pragma unroll
   for (int i = 0; i < CPR; ++i) {
-    const int r = (lane + 32 * i) / CPR, c = (lane + 32 * i) % CPR;
+    const int r = (lane + 32 * i) / CPR, cc = (lane + 32 * i) % CPR;
     const int vr = (r & ~7) | ((r & 7) >> 1) | ((r & 1) << 2);
-    const bool in = whole || j0 + r < T_cap;
-    cp_async_16(dst + 16 * (lane + 32 * i), in ? k + 512 * i : kc, in ? 16u : 0u);
-    cp_async_16(dst + KdTile<D>::CODES + vr * (D / 2) + 16 * c, in ? v + 512 * i : vc, in ? 16u : 0u);
+    const uint32_t kd = dst + 16 * (lane + 32 * i), vd = dst + KdTile<D>::CODES + vr * (D / 2) + 16 * cc;
+    if (j0 + KD_KT <= T_cap) {
+      cp_async_16(kd, kc + off + 512 * i, 16u);
+      cp_async_16(vd, vc + off + 512 * i, 16u);
+    } else {
+      const bool in = j0 + r < T_cap;
+      cp_async_16(kd, in ? kc + off + 512 * i : kc, in ? 16u : 0u);
+      cp_async_16(vd, in ? vc + off + 512 * i : vc, in ? 16u : 0u);
+    }
   }
   if (lane < 16) {
-    const int c = lane & 7;                          // 4 steps a chunk (T_cap is a multiple of 16)
-    const bool in = whole || j0 + 4 * c < T_cap;
-    const float* src = lane < 8 ? ks : vs;
-    cp_async_16(dst + 2 * KdTile<D>::CODES + (lane < 8 ? 0 : KD_KT * 4) + 16 * c, in ? src + j0 + 4 * c : src,
-                in ? 16u : 0u);
+    const bool in = j0 + 4 * c < T_cap;
+    cp_async_16(steps_dst, in ? steps : ks, in ? 16u : 0u);
   }
 }
 
 template <int D, int NT, typename XT>
-__global__ void __launch_bounds__(32 * KD_WARPS)
+__global__ void __launch_bounds__(32 * KD_WARPS, NT == 1 && sizeof(XT) == 2 ? 4 : 1)
 kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e) {
   constexpr bool SPLIT = sizeof(XT) == 4;            // fp32: two fp16 terms for q and for the weights
   constexpr int ROWS = 8 * NT;
@@ -200,20 +204,21 @@ kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e) {
       kd_stage<D>(kc, ks, vc, vs, tiles.at(first + i * stride) * KD_KT, s.T_cap, ring_a + i * KdTile<D>::BYTES, lane);
     cp_async_commit();
   }
-  for (int it = 0; it < mine; ++it) {
+  int slot = 0, nslot = KD_STAGES - 1;               // stages of this tile and of the one that is fetched
+#pragma unroll 1
+  for (int it = 0, at = first; it < mine; ++it, at += stride) {
     asm volatile("cp.async.wait_group %0;" :: "n"(KD_STAGES - 2) : "memory");
     __syncwarp();                                    // this tile is in place, and every lane is done with the last one
-    {
-      const int nx = it + KD_STAGES - 1;
-      if (nx < mine)
-        kd_stage<D>(kc, ks, vc, vs, tiles.at(first + nx * stride) * KD_KT, s.T_cap,
-                    ring_a + (nx % KD_STAGES) * KdTile<D>::BYTES, lane);
-      cp_async_commit();
-    }
-    const uint8_t* stage = ring + (it % KD_STAGES) * KdTile<D>::BYTES;
+    if (it + KD_STAGES - 1 < mine)
+      kd_stage<D>(kc, ks, vc, vs, tiles.at(at + (KD_STAGES - 1) * stride) * KD_KT, s.T_cap,
+                  ring_a + nslot * KdTile<D>::BYTES, lane);
+    cp_async_commit();
+    const uint8_t* stage = ring + slot * KdTile<D>::BYTES;
+    slot = slot + 1 == KD_STAGES ? 0 : slot + 1;
+    nslot = nslot + 1 == KD_STAGES ? 0 : nslot + 1;
     const float* kst = reinterpret_cast<const float*>(stage + 2 * KdTile<D>::CODES);
     const float* vst = kst + KD_KT;
-    const int j0 = tiles.at(first + it * stride) * KD_KT;
+    const int j0 = tiles.at(at) * KD_KT;
     // ---- scores of keys 16 x + g, + 8 (rows) and queries 2t, 2t + 1 (columns) ----
     // (fp32: the products of the second terms are summed apart, so that the first ones' sum is cut
     // off half as often)
@@ -296,7 +301,7 @@ kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e) {
       }
     // ---- running maximum (a query's keys lie in the 8 lanes of one t), weights, sums ----
     bool moved = false;
-    float corr[NT][2];
+    float last[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -305,19 +310,19 @@ kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e) {
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        const float mn = fmaxf(m[n][i], mx);
-        corr[n][i] = m[n][i] == mn ? 1.f : ex2(m[n][i] - mn);
-        moved |= m[n][i] != mn;
-        m[n][i] = mn;
+        last[n][i] = m[n][i];
+        m[n][i] = fmaxf(mx, m[n][i]);
+        moved |= m[n][i] != last[n][i];
       }
     if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          l[n][i] *= corr[n][i];
+          const float corr = m[n][i] == last[n][i] ? 1.f : ex2(last[n][i] - m[n][i]);
+          l[n][i] *= corr;
 #pragma unroll
-          for (int q = 0; q < MT; ++q) { o[n][q][i] *= corr[n][i]; o[n][q][2 + i] *= corr[n][i]; }
+          for (int q = 0; q < MT; ++q) { o[n][q][i] *= corr; o[n][q][2 + i] *= corr; }
         }
     }
     uint32_t ph[2][NT][2], pr[SPLIT ? 2 : 1][SPLIT ? NT : 1][2];
