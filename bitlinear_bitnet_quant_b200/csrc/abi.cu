@@ -48,8 +48,9 @@ cudaError_t run_append(const KvStep& s, const AppendArgs& a, int x_bf16, int d, 
 cudaError_t run_kv4_read(const KvStep& s, int kv_heads, int d, const uint8_t* Kc, const float* Ks, const uint8_t* Vc,
                          const float* Vs, void* K, void* V, int bf16, cudaStream_t st);
 bool kv4_prefill_applies(const KvStep& s, const AttnArgs& a, int bf16);
-size_t kv4_prefill_workspace(const KvStep& s, const AttnArgs& a, int d);
-cudaError_t run_kv4_prefill(const KvStep& s, const AttnArgs& a, int d, void* ws, size_t ws_bytes, cudaStream_t st);
+size_t kv4_prefill_workspace(const KvStep& s, const AttnArgs& a, int bf16, int d);
+cudaError_t run_kv4_prefill(const KvStep& s, const AttnArgs& a, int bf16, int d, void* ws, size_t ws_bytes,
+                            cudaStream_t st);
 cudaError_t run_kv4_decode(const KvStep& s, const AttnArgs& a, int bf16, int d, cudaStream_t st);
 }  // namespace bitnet
 
@@ -560,7 +561,7 @@ size_t bitnet_kv4_attention_workspace_size(int dtype, int64_t B, int64_t L, int 
   if (t_max > 0) s.limit = (int)t_max;
   const bitnet::AttnArgs a = kv4_attention_args(heads, kv_heads, window, sinks);
   if (B == 0 || L == 0 || !bitnet::kv4_prefill_applies(s, a, dtype == BITNET_BF16)) return 0;
-  return bitnet::kv4_prefill_workspace(s, a, head_dim);
+  return bitnet::kv4_prefill_workspace(s, a, dtype == BITNET_BF16, head_dim);
 }
 
 int bitnet_kv4_attention(const void* Q, int dtype, const uint8_t* Kc, const float* Ks, const uint8_t* Vc,
@@ -584,12 +585,12 @@ int bitnet_kv4_attention(const void* Q, int dtype, const uint8_t* Kc, const floa
   a.Vs = Vs;
   a.A = A;
   const bool prefill = bitnet::kv4_prefill_applies(s, a, dtype == BITNET_BF16);
-  if (prefill && (!workspace || workspace_bytes < bitnet::kv4_prefill_workspace(s, a, head_dim)))
+  if (prefill && (!workspace || workspace_bytes < bitnet::kv4_prefill_workspace(s, a, dtype == BITNET_BF16, head_dim)))
     return BITNET_ERR_WORKSPACE;
   const int d = check_device();
   if (d != BITNET_OK) return d;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return cuda_status(prefill ? bitnet::run_kv4_prefill(s, a, head_dim, workspace, workspace_bytes, st)
+  return cuda_status(prefill ? bitnet::run_kv4_prefill(s, a, dtype == BITNET_BF16, head_dim, workspace, workspace_bytes, st)
                              : bitnet::run_kv4_decode(s, a, dtype == BITNET_BF16, head_dim, st));
 }
 

@@ -410,7 +410,7 @@ kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e) {
     float sum = 0.f;
 #pragma unroll
     for (int w = 0; w < KD_WARPS; ++w) {
-      const float c = w_m[w][tid] == -INFINITY ? 0.f : ex2(w_m[w][tid] - mx);
+      const float c = w_m[w][tid] == -INFINITY && w_l[w][tid] == 0.f ? 0.f : ex2(w_m[w][tid] - mx);
       sum += w_l[w][tid] * c;
       w_m[w][tid] = c;                               // the warp's factor
     }
@@ -439,14 +439,14 @@ kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e) {
     for (uint32_t c = 0; c < csize; ++c) mx = fmaxf(mx, ld_cluster_f32(cluster_map(m_a + 4 * row, c)));
     float sum = 0.f, x0 = 0.f, x1 = 0.f;
     for (uint32_t c = 0; c < csize; ++c) {
-      const float mc = ld_cluster_f32(cluster_map(m_a + 4 * row, c));
-      const float w = mc == -INFINITY ? 0.f : ex2(mc - mx);
-      sum += w * ld_cluster_f32(cluster_map(l_a + 4 * row, c));
+      const float mc = ld_cluster_f32(cluster_map(m_a + 4 * row, c)), lc = ld_cluster_f32(cluster_map(l_a + 4 * row, c));
+      const float w = mc == -INFINITY && lc == 0.f ? 0.f : ex2(mc - mx);
+      sum += w * lc;
       const uint32_t oa = cluster_map(o_a + 4 * (row * D + dim), c);
       x0 += w * ld_cluster_f32(oa);
       x1 += w * ld_cluster_f32(oa + 4);
     }
-    const float r = mx == -INFINITY ? 0.f : 1.0f / sum;    // a query that sees no key: zeros
+    const float r = mx == -INFINITY && sum == 0.f ? 0.f : 1.0f / sum;    // a query that sees no key: zeros
     const int R = r0 + row, tok = R / group;
     const int64_t off = (((int64_t)b * s.L + tok) * a.heads + h * group + R - tok * group) * D + dim;
     if constexpr (SPLIT) {

@@ -28,6 +28,10 @@ constexpr int KP_POLY = 4;                           // every KP_POLY-th pair's 
 // 2^r on [-1/2, 1/2], the cubic of least largest relative error (7.5e-05), by linear programming
 constexpr float EXP2_C0 = 0.999928073f, EXP2_C1 = 0.693260985f, EXP2_C2 = 0.242611125f, EXP2_C3 = 0.055171670f;
 
+// fp32 rows: of every key of a tile, 4 arrays of KP_KT: the score's factor, the exponent e
+// of its value step f 2^e, 2^-e (0 where no query sees the key) and f.
+constexpr int KP_KEY_FLOATS = 4 * KP_KT;
+
 template <int D>
 struct KpTile {
   static constexpr int BYTES = KP_KT * D * 2;        // keys or values of a tile
@@ -104,10 +108,12 @@ BN_DEV KpSeen kp_seen(const KvStep& s, int b) {
 // Expansion: a block a tile and key head; four warps its keys, four its values.  Bound
 // by memory (reads D + 8 bytes a key and head, writes 4 D).
 // ---------------------------------------------------------------------------
-template <int D>
+// EXACT (fp32 rows): the images hold the codes themselves, and for every key the factors
+// of KpKey are written instead of the tile's.
+template <int D, bool EXACT>
 __global__ void __launch_bounds__(256)
 kv4_expand_kernel(const KvStep s, const AttnArgs a, int head0, int slots, float scale_log2e, uint8_t* images,
-                  float2* factors) {
+                  float* factors) {
   using M = KpTile<D>;
   __shared__ __align__(16) uint32_t step_top[2][4];
   pdl_launch_dependents();
@@ -141,39 +147,60 @@ kv4_expand_kernel(const KvStep s, const AttnArgs a, int head0, int slots, float 
     vstep = ldg_f32(a.Vs + (int64_t)head * s.T_cap + j0 + key);
   }
   const bool bad = !(fabsf(kstep) < INFINITY && fabsf(vstep) < INFINITY);
-  const uint32_t kt = __reduce_max_sync(0xffffffffu, bad ? 0u : __float_as_uint(fabsf(kstep)));
-  const uint32_t vt = __reduce_max_sync(0xffffffffu, bad ? 0u : __float_as_uint(fabsf(vstep)));
-  if (warp < 4 && lane == 0) {
-    step_top[0][warp] = kt;
-    step_top[1][warp] = vt;
-  }
-  __syncthreads();
-  const uint4 k4 = *reinterpret_cast<const uint4*>(step_top[0]), v4 = *reinterpret_cast<const uint4*>(step_top[1]);
-  const int E = row_exponent(__uint_as_float(max(max(k4.x, k4.y), max(k4.z, k4.w))));
-  const int F = step_exponent(__uint_as_float(max(max(v4.x, v4.y), max(v4.z, v4.w))));
-  const float step = val ? vstep * pow2i(11 - F) : kstep * pow2i(11 - E);
-  // 8 bits of the step times a code are exact in fp16; the rest of the step joins in one rounding
-  const float top = __uint_as_float(__float_as_uint(step) & 0xFFFF0000u);
-  const uint32_t sh = bad ? (val ? 0u : 0x7FFF7FFFu) : both_halves(top), sl = bad ? 0u : both_halves(step - top);
   const int64_t tile = (int64_t)blockIdx.y * slots + slot;
+  uint32_t sh = 0u, sl = 0u;                         // a row's step in two fp16 terms
+  if constexpr (EXACT) {
+    if (!val) {
+      float* f = factors + tile * KP_KEY_FLOATS + key;
+      const int e = step_exponent(vstep);
+      const float inv = pow2i(-e);
+      const bool shown = is_seen(j0 + key);
+      f[0] = bad ? NAN : kstep * scale_log2e;
+      f[KP_KT] = (float)e;
+      f[2 * KP_KT] = bad || !shown ? 0.f : inv;
+      f[3 * KP_KT] = bad ? 0.f : vstep * inv;
+    }
+  } else {
+    const uint32_t kt = __reduce_max_sync(0xffffffffu, bad ? 0u : __float_as_uint(fabsf(kstep)));
+    const uint32_t vt = __reduce_max_sync(0xffffffffu, bad ? 0u : __float_as_uint(fabsf(vstep)));
+    if (warp < 4 && lane == 0) {
+      step_top[0][warp] = kt;
+      step_top[1][warp] = vt;
+    }
+    __syncthreads();
+    const uint4 k4 = *reinterpret_cast<const uint4*>(step_top[0]), v4 = *reinterpret_cast<const uint4*>(step_top[1]);
+    const int E = row_exponent(__uint_as_float(max(max(k4.x, k4.y), max(k4.z, k4.w))));
+    const int F = step_exponent(__uint_as_float(max(max(v4.x, v4.y), max(v4.z, v4.w))));
+    const float step = val ? vstep * pow2i(11 - F) : kstep * pow2i(11 - E);
+    // 8 bits of the step times a code are exact in fp16; the rest of the step joins in one rounding
+    const float top = __uint_as_float(__float_as_uint(step) & 0xFFFF0000u);
+    sh = bad ? (val ? 0u : 0x7FFF7FFFu) : both_halves(top);
+    sl = bad ? 0u : both_halves(step - top);
+    if (tid == 0) reinterpret_cast<float2*>(factors)[tile] = make_float2(scale_log2e * pow2i(E - 11), (float)F);
+  }
   uint8_t* dst = images + tile * M::PAIR + val * M::BYTES + (key & 96) * 128;
 #pragma unroll
   for (int q = 0; q < PARTS; ++q) {
     const int row = row0 + RPI * q;
-    const uint32_t rh = __shfl_sync(0xffffffffu, sh, row), rl = __shfl_sync(0xffffffffu, sl, row);
+    uint32_t rh = 0u, rl = 0u;
+    if constexpr (!EXACT) {
+      rh = __shfl_sync(0xffffffffu, sh, row);
+      rl = __shfl_sync(0xffffffffu, sl, row);
+    }
     const uint32_t words[4] = {cw[q].x, cw[q].y, cw[q].z, cw[q].w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       uint32_t v[4];
       codes_to_half2(words[e], v);
+      if constexpr (!EXACT) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = h2_fma(v[j], rl, h2_mul(v[j], rh));
+        for (int j = 0; j < 4; ++j) v[j] = h2_fma(v[j], rl, h2_mul(v[j], rh));
+      }
       const int chunk = 4 * (part & 1) + e;
       *reinterpret_cast<uint4*>(dst + (part >> 1) * 16384 + row * 128 + ((chunk ^ (row & 7)) << 4)) =
           make_uint4(v[0], v[1], v[2], v[3]);
     }
   }
-  if (tid == 0) factors[tile] = make_float2(scale_log2e * pow2i(E - 11), (float)F);
 }
 
 // ---------------------------------------------------------------------------
@@ -296,7 +323,8 @@ BN_DEV KpRows kp_rows(int r0, int n_rows, int group, int64_t p0, int limit) {
 template <int D>
 __global__ void __launch_bounds__(KP_THREADS, 1)
 kv4_prefill_kernel(const KvStep s, const AttnArgs a, int head0, int heads_here, int row_tiles, int slots,
-                   const uint8_t* __restrict__ images, const float2* __restrict__ factors) {
+                   const uint8_t* __restrict__ images, const float* __restrict__ tile_factors) {
+  const float2* factors = reinterpret_cast<const float2*>(tile_factors);
   using M = KpSmem<D>;
   constexpr float BIAS = 7.f, MOVE = 8.f;
   constexpr uint32_t S_COL = 0, O_COL = 256;         // streams: + 128 g
@@ -457,7 +485,7 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, int head0, int heads_here, 
       // ---- the output, divided by the sum ----
       if (ok && used > 0) ok = kp_wait(&all_done, 0, DEV_ERR_TIMEOUT_ACC);
       tc_fence_after();
-      const float inv = m == -INFINITY ? 0.f : 0x1p-11f / l;           // a query that sees no key: zeros
+      const float inv = m == -INFINITY && l == 0.f ? 0.f : 0x1p-11f / l;      // a query that sees no key: zeros
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.A) + off;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
@@ -561,6 +589,348 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, int head0, int heads_here, 
 }
 
 // ---------------------------------------------------------------------------
+// fp32 rows.  What the sums may lose is 2^-22 here, so every fp32 operand is two fp16
+// terms (22 bits) against the codes, which are exact; the steps stay in the softmax, as
+// in the few-query kernel: with step_v = f 2^e a key's exponent takes e, the operand is
+// p f, the sum takes p 2^-e.  The tensor cores cut their sums off (measured: 1e-7 of the
+// sum a product of 16 values deep, 5e-5 after 512), so a tile's output is summed there
+// and the tiles' with rounding outside.
+//
+// A block takes 128 rows of one key head.  Even and odd key tiles go to two groups of
+// four warps, each with its own scores buffer, maximum and sum; a tile's output is
+// written to a third buffer of tensor memory and added to the running one, a fourth, by
+// four more warps, with the maxima's factors.  Per tile 4 x 8 products of 128 x 128 x 16
+// (2048 cycles), which bound it.
+// ---------------------------------------------------------------------------
+constexpr int KX_THREADS = 448;                      // weights: warps 0-3, 4-7; sums: 8-11; products: 12; copies: 13
+constexpr int KX_RING = 4;                           // tiles whose keys' factors are held
+
+template <int D>
+struct KxSmem {
+  static constexpr int TILE = KpTile<D>::BYTES;
+  static constexpr int Q = 0, K = 2 * TILE, V = 4 * TILE, KEYS = 6 * TILE;             // q: both terms; 2 of K and V
+  static constexpr int BYTES = KEYS + KX_RING * KP_KEY_FLOATS * 4 + 1024;
+};
+
+template <int D>
+__global__ void __launch_bounds__(KX_THREADS, 1)
+kv4_prefill_f32_kernel(const KvStep s, const AttnArgs a, int head0, int heads_here, int row_tiles, int slots,
+                       const uint8_t* __restrict__ images, const float* __restrict__ factors) {
+  using M = KxSmem<D>;
+  constexpr float BIAS = 10.f;
+  constexpr uint32_t S_COL = 0, PART = 256, SUM = 384;          // scores: + 128 g
+  extern __shared__ uint8_t kp_raw[];
+  __shared__ uint64_t q_full, k_full[2], v_full[2], k_empty[2], v_empty[2], key_full[KX_RING], s_full[2], p_full[2],
+      part_full, part_free, all_done;
+  __shared__ uint32_t tmem_sh;
+  __shared__ int failed;
+  __shared__ float tile_m[4][128], fin_m[2][128], fin_l[2][128];
+  uint8_t* sm = smem_align(kp_raw, 1024);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  if (tid == 0) {
+    mbar_init(&q_full, 128);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&v_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 128);
+    }
+    for (int i = 0; i < KX_RING; ++i) mbar_init(&key_full[i], 1);
+    mbar_init(&part_full, 1);
+    mbar_init(&part_free, 128);
+    mbar_init(&all_done, 1);
+    failed = 0;
+    fence_barrier_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(&tmem_sh, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_sh;
+  // only once the tensor memory is allocated may the next kernel of the stream be scheduled
+  pdl_launch_dependents();
+  pdl_wait();                                        // q, the cache and the images come from the previous kernels
+
+  const int rt = row_tiles - 1 - (int)(blockIdx.x / heads_here);       // the longest row tiles first
+  const int here = (int)(blockIdx.x % heads_here), b = (head0 + here) / a.kv_heads, h = head0 + here - b * a.kv_heads;
+  const int group = a.heads / a.kv_heads;
+  const int n_rows = kv_real_tokens(s, b) * group;
+  const int r0 = rt * 128;
+  const int64_t p0 = kv_first_position(s, b);
+  const KpRows rows = kp_rows(r0, n_rows, group, p0, s.limit);
+  KeyTiles tiles = {0, 0, 0};
+  if (rows.n > 0) tiles = key_tiles<KP_KT>(rows.p_lo, rows.p_hi, a.window, a.sinks);
+  const KpSeen seen = kp_seen(s, b);
+  const KeyTiles all = key_tiles<KP_KT>(seen.first, seen.last, a.window, a.sinks);
+  auto slot = [&](int i) {
+    const int j = tiles.at(i);
+    return (int64_t)here * slots + (j < all.sink_tiles ? j : j - all.first + all.sink_tiles);
+  };
+  const int row = tid & 127;
+  const int R = r0 + row, tok = R / group;
+  const bool real = R < n_rows;
+  const int64_t off = (((int64_t)b * s.L + tok) * a.heads + h * group + R - tok * group) * D;
+  const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+  const bool work = r0 < n_rows;
+  bool ok = true;
+  float sum_m = -INFINITY;                           // the running output's maximum (warps 8-11)
+
+  if (work && warp < 8) {
+    // ------------------------------------------------ scores to weights, one row a thread
+    const int g = warp >> 2;
+    const int64_t pr = p0 + tok;
+    const int p = !real ? rows.p_hi : pr >= 0 && pr < s.limit ? (int)pr : -1;      // padding rows see what their tile does
+    const float* src = static_cast<const float*>(a.Q) + off;
+    float mx = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < D / 4; ++c) {
+      const uint4 v = real ? ldg_v4(src + 4 * c) : make_uint4(0u, 0u, 0u, 0u);
+      const float x[4] = {fabsf(__uint_as_float(v.x)), fabsf(__uint_as_float(v.y)), fabsf(__uint_as_float(v.z)),
+                          fabsf(__uint_as_float(v.w))};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) mx = fmaxf(mx, x[j] < INFINITY ? x[j] : 0.f);
+    }
+    const int e = row_exponent(mx);
+    const float up = pow2i(14 - e), row_scale = pow2i(e - 14);
+    if (g == 0) {
+      uint8_t* dst = sm + M::Q + row * 128;
+#pragma unroll 2
+      for (int c = 0; c < D / 8; ++c) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint4 v = real ? ldg_v4(src + 8 * c + 4 * k) : make_uint4(0u, 0u, 0u, 0u);
+          const float x0 = __uint_as_float(v.x) * up, x1 = __uint_as_float(v.y) * up;
+          const float x2 = __uint_as_float(v.z) * up, x3 = __uint_as_float(v.w) * up;
+          hi[2 * k] = pack_half2(x0, x1);
+          hi[2 * k + 1] = pack_half2(x2, x3);
+          lo[2 * k] = half2_rest(hi[2 * k], x0, x1);
+          lo[2 * k + 1] = half2_rest(hi[2 * k + 1], x2, x3);
+        }
+        uint8_t* at = dst + (c >> 3) * 16384 + (((c & 7) ^ (row & 7)) << 4);
+        *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(at + M::TILE) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&q_full);
+    }
+    const uint32_t S = lanes + S_COL + 128u * g;
+    const uint64_t rs2 = pack_f2(row_scale, row_scale);
+    float m = -INFINITY, l = 0.f;
+    for (int i = g, n = 0; i < tiles.count && ok; i += 2, ++n) {
+      const int j0 = tiles.at(i) * KP_KT;
+      const bool masked = !rows.full(j0, KP_KT, a.window, a.sinks);
+      const int hi = p - j0, lo = a.window > 0 ? p - a.window - j0 : -1, sk = a.sinks - j0;
+      ok = kp_wait(&key_full[i % KX_RING], (i / KX_RING) & 1, DEV_ERR_TIMEOUT_FULL) &&
+           kp_wait(&s_full[g], n & 1, DEV_ERR_TIMEOUT_ACC);
+      if (!ok) break;
+      tc_fence_after();
+      const float* ks = reinterpret_cast<const float*>(sm + M::KEYS) + (i % KX_RING) * KP_KEY_FLOATS;
+      // 32 scores as base-2 exponents, the value step's among them
+      auto scores = [&](int c, float (&x)[32]) {
+        float zero = 0.f, one = 0.f;
+        tmem_ld32(S + 32 * c, reinterpret_cast<uint32_t*>(x));
+        kp_loads_done(zero, one);
+        const uint64_t rs = add_f2(rs2, pack_f2(zero, one));           // (after the load)
+#pragma unroll
+        for (int q = 0; q < 32; q += 4) {
+          const ulonglong2 kf = *reinterpret_cast<const ulonglong2*>(ks + 32 * c + q);
+          const ulonglong2 ef = *reinterpret_cast<const ulonglong2*>(ks + KP_KT + 32 * c + q);
+          unpack_f2(fma_f2(pack_f2(x[q], x[q + 1]), mul_f2(kf.x, rs), ef.x), x[q], x[q + 1]);
+          unpack_f2(fma_f2(pack_f2(x[q + 2], x[q + 3]), mul_f2(kf.y, rs), ef.y), x[q + 2], x[q + 3]);
+        }
+        if (masked) {
+#pragma unroll
+          for (int q = 0; q < 32; ++q)
+            x[q] = 32 * c + q <= hi && (32 * c + q > lo || 32 * c + q < sk) ? x[q] : -INFINITY;
+        }
+      };
+      float top = -INFINITY;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        float x[32];
+        scores(c, x);
+#pragma unroll
+        for (int q = 0; q < 32; q += 2) top = max3(top, x[q], x[q + 1]);
+      }
+      const float mn = fmaxf(m, top);
+      l *= m == mn ? 1.f : ex2(m - mn);
+      m = mn;
+      const float ref = m == -INFINITY ? 0.f : BIAS - m;
+      const uint64_t ref2 = pack_f2(ref, ref);
+      uint64_t l2 = 0;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        float x[32];
+        uint32_t w[32];                              // 16 pairs, then what they leave
+        scores(c, x);
+#pragma unroll
+        for (int q = 0; q < 32; q += 4) {
+          const ulonglong2 inv = *reinterpret_cast<const ulonglong2*>(ks + 2 * KP_KT + 32 * c + q);
+          const ulonglong2 vf = *reinterpret_cast<const ulonglong2*>(ks + 3 * KP_KT + 32 * c + q);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float e0, e1, w0, w1;
+            unpack_f2(add_f2(pack_f2(x[q + 2 * k], x[q + 2 * k + 1]), ref2), e0, e1);
+            const uint64_t e2 = pack_f2(ex2(e0), ex2(e1));
+            l2 = fma_f2(e2, k == 0 ? inv.x : inv.y, l2);
+            unpack_f2(mul_f2(e2, k == 0 ? vf.x : vf.y), w0, w1);
+            w[q / 2 + k] = pack_half2(w0, w1);
+            w[16 + q / 2 + k] = half2_rest(w[q / 2 + k], w0, w1);
+          }
+        }
+        tmem_st32(S + 32 * c, w);                    // over the scores they come from
+      }
+      float l0, l1;
+      unpack_f2(l2, l0, l1);
+      l += l0 + l1;
+      tile_m[i & 3][row] = m;
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&p_full[g]);
+    }
+    fin_m[g][row] = m;
+    fin_l[g][row] = l;
+  } else if (work && warp < 12) {
+    // ------------------------------------------------ the tiles' outputs into the running one
+    for (int i = 0; i < tiles.count && ok; ++i) {
+      ok = kp_wait(&part_full, i & 1, DEV_ERR_TIMEOUT_ACC);
+      if (!ok) break;
+      tc_fence_after();
+      const float mt = tile_m[i & 3][row], mn = fmaxf(sum_m, mt);
+      float keep = sum_m == mn ? 1.f : ex2(sum_m - mn), add = mt == mn ? 1.f : ex2(mt - mn);
+      if (mn == -INFINITY) keep = add = 0.f;
+      sum_m = mn;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        float x[32], y[32];
+        tmem_ld32(lanes + PART + c, reinterpret_cast<uint32_t*>(x));
+        if (i > 0) tmem_ld32(lanes + SUM + c, reinterpret_cast<uint32_t*>(y));
+        kp_loads_done(keep, add);
+#pragma unroll
+        for (int q = 0; q < 32; ++q) y[q] = i > 0 ? y[q] * keep + x[q] * add : x[q] * add;
+        tmem_st32(lanes + SUM + c, reinterpret_cast<uint32_t (&)[32]>(y));
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&part_free);
+    }
+  } else if (work && warp == 12 && tiles.count > 0) {
+    // ------------------------------------------------ products
+    constexpr uint32_t ID_S = idesc_f16(128, KP_KT, false, false), ID_O = idesc_f16(128, D, false, true);
+    ok = kp_wait(&q_full, 0, DEV_ERR_TIMEOUT_A);
+    const uint32_t qd = desc_lo(smem_u32(sm + M::Q)), kd = desc_lo(smem_u32(sm + M::K)), vd = desc_lo(smem_u32(sm + M::V));
+    for (int i = 0; i < tiles.count + 2 && ok; ++i) {
+      if (i >= 2) {                                  // the output of tile i - 2, whose weights lie where tile i's scores go
+        const int t = i - 2;
+        ok = kp_wait(&v_full[t & 1], (t >> 1) & 1, DEV_ERR_TIMEOUT_FULL) &&
+             kp_wait(&p_full[t & 1], (t >> 1) & 1, DEV_ERR_TIMEOUT_ACC) &&
+             (t == 0 || kp_wait(&part_free, (t - 1) & 1, DEV_ERR_TIMEOUT_ACC));
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t P = tmem + S_COL + 128u * (t & 1), vb = vd + (t & 1) * (M::TILE >> 4);
+#pragma unroll
+          for (int term = 1; term >= 0; --term)      // the small terms first
+#pragma unroll
+            for (int k = 0; k < KP_KT / 16; ++k)
+              mma_f16_ts(tmem + PART, P + 32 * (k >> 1) + 16 * term + 8 * (k & 1), vb + (2048 >> 4) * k, ID_O,
+                         term == 0 || k > 0);
+          mma_commit(&part_full);
+          mma_commit(&v_empty[t & 1]);
+        }
+        __syncwarp();
+      }
+      if (i < tiles.count) {
+        ok = kp_wait(&k_full[i & 1], (i >> 1) & 1, DEV_ERR_TIMEOUT_FULL);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t kb = kd + (i & 1) * (M::TILE >> 4);
+#pragma unroll
+          for (int term = 1; term >= 0; --term)
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t o = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+              mma_f16_ss(tmem + S_COL + 128u * (i & 1), qd + term * (M::TILE >> 4) + o, kb + o, ID_S, term == 0 || k > 0);
+            }
+          mma_commit(&s_full[i & 1]);
+          mma_commit(&k_empty[i & 1]);
+        }
+        __syncwarp();
+      }
+    }
+    // completion of everything issued, also after a wait that gave up
+    if (elect_one()) mma_commit(&all_done);
+    __syncwarp();
+    mbar_wait(&all_done, 0, DEV_ERR_TIMEOUT_ACC, false);
+  } else if (work && warp == 13) {
+    // ------------------------------------------------ copies
+    int i = 0;
+    for (; i < tiles.count && ok; ++i) {
+      const uint8_t* src = images + slot(i) * (2 * M::TILE);
+      const int st = i & 1, ring = i % KX_RING;
+      if (i >= 2) ok = kp_wait(&k_empty[st], ((i >> 1) - 1) & 1, DEV_ERR_TIMEOUT_EMPTY);
+      if (ok && elect_one()) {
+        // (tile i - 4's factors: its weights were used before the scores of tile i - 2 were issued)
+        mbar_arrive_expect_tx(&key_full[ring], KP_KEY_FLOATS * 4);
+        bulk_load(sm + M::KEYS + ring * KP_KEY_FLOATS * 4, factors + slot(i) * KP_KEY_FLOATS, KP_KEY_FLOATS * 4,
+                  &key_full[ring]);
+        mbar_arrive_expect_tx(&k_full[st], M::TILE);
+        bulk_load(sm + M::K + st * M::TILE, src, M::TILE, &k_full[st]);
+      }
+      __syncwarp();
+      if (i >= 2 && ok) ok = kp_wait(&v_empty[st], ((i >> 1) - 1) & 1, DEV_ERR_TIMEOUT_EMPTY);
+      if (ok && elect_one()) {
+        mbar_arrive_expect_tx(&v_full[st], M::TILE);
+        bulk_load(sm + M::V + st * M::TILE, src + M::TILE, M::TILE, &v_full[st]);
+      }
+      __syncwarp();
+    }
+  }
+  if (!ok) failed = 1;
+  __syncthreads();
+  if (work && warp >= 8 && warp < 12 && !failed) {
+    tc_fence_after();
+    // the two groups' sums in the running output's scale
+    float sum = 0.f;
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+      if (fin_m[g][row] != -INFINITY || fin_l[g][row] != 0.f) sum += fin_l[g][row] * ex2(fin_m[g][row] - sum_m);
+    float inv = sum_m == -INFINITY && sum == 0.f ? 0.f : 1.0f / sum;   // a query that sees no key: zeros
+    float* out = static_cast<float*>(a.A) + off;
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+      float x[32], none = 0.f;
+      if (tiles.count > 0) {
+        tmem_ld32(lanes + SUM + c, reinterpret_cast<uint32_t*>(x));
+        kp_loads_done(inv, none);
+      }
+      if (real) {
+#pragma unroll
+        for (int q = 0; q < 32; q += 4) {
+          float y[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) y[j] = inv == 0.f ? 0.f : x[q + j] * inv;
+          *reinterpret_cast<float4*>(out + c + q) = make_float4(y[0], y[1], y[2], y[3]);
+        }
+      }
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
 // Tiles of a sequence that a step's queries can see, at most.
@@ -571,37 +941,38 @@ static int64_t kp_slots(const KvStep& s, const AttnArgs& a) {
   return some < all ? some : all;
 }
 // Workspace of one key head: its tiles' images, then their factors (both in multiples of 16 bytes).
-static int64_t kp_head_bytes(const KvStep& s, const AttnArgs& a, int d) {
-  return kp_slots(s, a) * (2 * KP_KT * d * 2 + 16);
+static int64_t kp_head_bytes(const KvStep& s, const AttnArgs& a, int bf16, int d) {
+  return kp_slots(s, a) * (2 * KP_KT * d * 2 + (bf16 ? 16 : KP_KEY_FLOATS * 4));
 }
 // Enough for one launch of every head, or 256 MB: heads are then taken in turns.
-size_t kv4_prefill_workspace(const KvStep& s, const AttnArgs& a, int d) {
-  const int64_t head = kp_head_bytes(s, a, d), heads = (int64_t)a.kv_heads * s.B, most = (int64_t)256 << 20;
+size_t kv4_prefill_workspace(const KvStep& s, const AttnArgs& a, int bf16, int d) {
+  const int64_t head = kp_head_bytes(s, a, bf16, d), heads = (int64_t)a.kv_heads * s.B, most = (int64_t)256 << 20;
   int64_t turn = most / head;
   turn = turn < 1 ? 1 : (turn < heads ? turn : heads);
   return (size_t)(turn * head);
 }
 
-template <int D>
+template <int D, bool EXACT>
 static cudaError_t launch_prefill(const KvStep& s, const AttnArgs& a, uint8_t* ws, size_t ws_bytes, cudaStream_t st) {
-  auto kern = kv4_prefill_kernel<D>;
-  constexpr size_t smem = KpSmem<D>::BYTES;
+  auto kern = EXACT ? kv4_prefill_f32_kernel<D> : kv4_prefill_kernel<D>;
+  constexpr size_t smem = EXACT ? KxSmem<D>::BYTES : KpSmem<D>::BYTES;
+  constexpr int THREADS = EXACT ? KX_THREADS : KP_THREADS, ROWS = EXACT ? 128 : 256;
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  const int row_tiles = (int)(((int64_t)s.L * (a.heads / a.kv_heads) + 255) / 256);
+  const int row_tiles = (int)(((int64_t)s.L * (a.heads / a.kv_heads) + ROWS - 1) / ROWS);
   const int slots = (int)kp_slots(s, a), heads = a.kv_heads * s.B;
-  const int64_t fit = (int64_t)ws_bytes / kp_head_bytes(s, a, D);
+  const int64_t fit = (int64_t)ws_bytes / kp_head_bytes(s, a, !EXACT, D);
   const int most = heads < 65535 ? heads : 65535;            // a grid dimension
   const int turn = (int)(fit < most ? fit : most);
   if (turn < 1) return cudaErrorInvalidValue;
-  float2* factors = reinterpret_cast<float2*>(ws + (int64_t)turn * slots * KpTile<D>::PAIR);
+  float* factors = reinterpret_cast<float*>(ws + (int64_t)turn * slots * KpTile<D>::PAIR);
   for (int head0 = 0; head0 < heads; head0 += turn) {
     const int n = heads - head0 < turn ? heads - head0 : turn;
-    e = launch_pdl(kv4_expand_kernel<D>, dim3((unsigned)slots, (unsigned)n), dim3(256), 0, st, 1u, s, a, head0, slots,
-                   (float)(1.4426950408889634 / sqrt((double)D)), ws, factors);
+    e = launch_pdl(kv4_expand_kernel<D, EXACT>, dim3((unsigned)slots, (unsigned)n), dim3(256), 0, st, 1u, s, a, head0,
+                   slots, (float)(1.4426950408889634 / sqrt((double)D)), ws, factors);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(kern, dim3((unsigned)(row_tiles * n)), dim3(KP_THREADS), smem, st, 1u, s, a, head0, n, row_tiles,
-                   slots, (const uint8_t*)ws, (const float2*)factors);
+    e = launch_pdl(kern, dim3((unsigned)(row_tiles * n)), dim3(THREADS), smem, st, 1u, s, a, head0, n, row_tiles, slots,
+                   (const uint8_t*)ws, (const float*)factors);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -609,12 +980,16 @@ static cudaError_t launch_prefill(const KvStep& s, const AttnArgs& a, uint8_t* w
 
 // Whether the step takes this path (the others need no workspace).
 bool kv4_prefill_applies(const KvStep& s, const AttnArgs& a, int bf16) {
-  return bf16 && (int64_t)s.L * (a.heads / a.kv_heads) >= 128;
+  (void)bf16;
+  return (int64_t)s.L * (a.heads / a.kv_heads) >= 128;
 }
 
-cudaError_t run_kv4_prefill(const KvStep& s, const AttnArgs& a, int d, void* ws, size_t ws_bytes, cudaStream_t st) {
+cudaError_t run_kv4_prefill(const KvStep& s, const AttnArgs& a, int bf16, int d, void* ws, size_t ws_bytes,
+                            cudaStream_t st) {
   uint8_t* w = static_cast<uint8_t*>(ws);
-  return d == 128 ? launch_prefill<128>(s, a, w, ws_bytes, st) : launch_prefill<64>(s, a, w, ws_bytes, st);
+  if (d == 128)
+    return bf16 ? launch_prefill<128, false>(s, a, w, ws_bytes, st) : launch_prefill<128, true>(s, a, w, ws_bytes, st);
+  return bf16 ? launch_prefill<64, false>(s, a, w, ws_bytes, st) : launch_prefill<64, true>(s, a, w, ws_bytes, st);
 }
 
 }  // namespace bitnet

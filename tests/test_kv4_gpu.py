@@ -333,6 +333,10 @@ def test_kv4_attention_hidden_values_do_not_leak():
             for l in (2, 3):
                 _check_attention(got[l:l + 1, 1:], q64.reshape(L, heads, d)[l:l + 1, 1:], k[0], v[0], np.array([l]), 1, 0,
                                  0, False)
+        # a query that sees NaN keys alone
+        cache.ks[0, 0, :2] = math.nan
+        A = api.bitnet_kv4_attention(rows(rng, L, heads * d, F32)[0], cache, 1, L, 0, heads)
+        assert A[:2].isnan().all()
         # every position outside the cache: zeros; some outside: those
         for first, zero in ((T, range(L)), (-L, range(L)), (T - 3, range(3, L)), (-2, range(2))):
             clean = rows(rng, L, heads * d, F32)[0]
