@@ -390,37 +390,42 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, int head0, int heads_here, 
       const int p = !real ? rows.p_hi : pr >= 0 && pr < s.limit ? (int)pr : -1;      // padding rows see what their tile does
       float row_scale;                               // base-2 score of an accumulator, up to the tile's factor
       {
-        // the row's values, scaled, K-major with 128-byte swizzle
-        uint8_t* dst = sm + M::Q + g * M::TILE + row * 128;
-        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.Q) + off;
-        uint4 v[D / 8];
-        float mx = 0.f;
+        // the warp's 32 rows, scaled, K-major with 128-byte swizzle.  RPL rows a load, each a run of
+        // lanes: a row a lane took 8000 cycles for its 32 lines a load
+        constexpr int LPR = D / 8, RPL = 32 / LPR;
+        const int lane = tid & 31, chunk = lane % LPR;
+        uint8_t* dst = sm + M::Q + g * M::TILE + (chunk >> 3) * 16384;
+        uint4 v[LPR];
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          v[c] = make_uint4(0u, 0u, 0u, 0u);
-          if (real) v[c] = ldg_v4(src + 8 * c);
+        for (int q = 0; q < LPR; ++q) {
+          const int from = RPL * q + lane / LPR;
+          const int64_t ro = __shfl_sync(0xffffffffu, off, from);
+          v[q] = make_uint4(0u, 0u, 0u, 0u);
+          if (__shfl_sync(0xffffffffu, (int)real, from)) v[q] = ldg_v4(static_cast<const __nv_bfloat16*>(a.Q) + ro + 8 * chunk);
         }
+        int my_e = 0;
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+        for (int q = 0; q < LPR; ++q) {
+          const uint32_t w[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
+          float mx = 0.f;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float lo = fabsf(bf16lo(w[j])), hi = fabsf(bf16hi(w[j]));
             mx = max3(mx, lo < INFINITY ? lo : 0.f, hi < INFINITY ? hi : 0.f);
           }
-        }
-        const int e = row_exponent(mx);
-        const float up = pow2i(14 - e);
-        row_scale = pow2i(e - 14);
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+          for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          const int e = row_exponent(mx);
+          const float up = pow2i(14 - e);
           uint32_t o[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) o[j] = pack_half2(bf16lo(w[j]) * up, bf16hi(w[j]) * up);
-          *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + (((c & 7) ^ (row & 7)) << 4)) =
-              make_uint4(o[0], o[1], o[2], o[3]);
+          const int at = (row & 96) + RPL * q + lane / LPR;
+          *reinterpret_cast<uint4*>(dst + at * 128 + (((chunk & 7) ^ (at & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+          const int er = __shfl_sync(0xffffffffu, e, (lane % RPL) * LPR);          // of row RPL q + lane % RPL
+          if (lane / RPL == q) my_e = er;
         }
+        row_scale = pow2i(my_e - 14);
         fence_proxy_async_smem();
         mbar_arrive(&q_full);
       }
@@ -485,28 +490,41 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, int head0, int heads_here, 
       // ---- the output, divided by the sum ----
       if (ok && used > 0) ok = kp_wait(&all_done, 0, DEV_ERR_TIMEOUT_ACC);
       tc_fence_after();
-      const float inv = m == -INFINITY && l == 0.f ? 0.f : 0x1p-11f / l;      // a query that sees no key: zeros
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.A) + off;
+      float inv = m == -INFINITY && l == 0.f ? 0.f : 0x1p-11f / l;      // a query that sees no key: zeros
+      // (through the queries' shared memory, free by now, to runs of lanes)
+      uint8_t* stage = sm + M::Q + g * M::TILE;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
-        uint32_t v[32];
+        float v[32], none = 0.f;
         if (used > 0) {
-          tmem_ld32(O + c, v);
-          tmem_wait_ld();
+          tmem_ld32(O + c, reinterpret_cast<uint32_t*>(v));
+          kp_loads_done(inv, none);
         }
-        if (real && ok) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t o[4];
+        for (int q = 0; q < 4; ++q) {
+          uint32_t o[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float y0 = inv == 0.f ? 0.f : __uint_as_float(v[8 * q + 2 * j]) * inv;
-              const float y1 = inv == 0.f ? 0.f : __uint_as_float(v[8 * q + 2 * j + 1]) * inv;
-              const __nv_bfloat162 hv = __floats2bfloat162_rn(y0, y1);
-              o[j] = *reinterpret_cast<const uint32_t*>(&hv);
-            }
-            *reinterpret_cast<uint4*>(out + c + 8 * q) = make_uint4(o[0], o[1], o[2], o[3]);
+          for (int j = 0; j < 4; ++j) {
+            const float y0 = inv == 0.f ? 0.f : v[8 * q + 2 * j] * inv, y1 = inv == 0.f ? 0.f : v[8 * q + 2 * j + 1] * inv;
+            const __nv_bfloat162 hv = __floats2bfloat162_rn(y0, y1);
+            o[j] = *reinterpret_cast<const uint32_t*>(&hv);
           }
+          const int chunk = c / 8 + q;
+          *reinterpret_cast<uint4*>(stage + (chunk >> 3) * 16384 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)) =
+              make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      }
+      __syncwarp();
+      {
+        constexpr int LPR = D / 8, RPL = 32 / LPR;
+        const int lane = tid & 31, chunk = lane % LPR;
+#pragma unroll 4
+        for (int q = 0; q < LPR; ++q) {
+          const int from = RPL * q + lane / LPR, at = (row & 96) + from;
+          const int64_t ro = __shfl_sync(0xffffffffu, off, from);
+          if (__shfl_sync(0xffffffffu, (int)(real && ok), from))
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.A) + ro + 8 * chunk) = *reinterpret_cast<const uint4*>(
+                stage + (chunk >> 3) * 16384 + at * 128 + (((chunk & 7) ^ (at & 7)) << 4));
         }
       }
       tc_fence_before();
@@ -623,12 +641,12 @@ kv4_prefill_f32_kernel(const KvStep s, const AttnArgs a, int head0, int heads_he
   __shared__ uint64_t q_full, k_full[2], v_full[2], k_empty[2], v_empty[2], key_full[KX_RING], s_full[2], p_full[2],
       part_full, part_free, all_done;
   __shared__ uint32_t tmem_sh;
-  __shared__ int failed;
+  __shared__ int failed, row_e[128];
   __shared__ float tile_m[4][128], fin_m[2][128], fin_l[2][128];
   uint8_t* sm = smem_align(kp_raw, 1024);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   if (tid == 0) {
-    mbar_init(&q_full, 128);
+    mbar_init(&q_full, 256);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], 1);
       mbar_init(&v_full[i], 1);
@@ -685,40 +703,38 @@ kv4_prefill_f32_kernel(const KvStep s, const AttnArgs a, int head0, int heads_he
     const int g = warp >> 2;
     const int64_t pr = p0 + tok;
     const int p = !real ? rows.p_hi : pr >= 0 && pr < s.limit ? (int)pr : -1;      // padding rows see what their tile does
-    const float* src = static_cast<const float*>(a.Q) + off;
-    float mx = 0.f;
-#pragma unroll 4
-    for (int c = 0; c < D / 4; ++c) {
-      const uint4 v = real ? ldg_v4(src + 4 * c) : make_uint4(0u, 0u, 0u, 0u);
-      const float x[4] = {fabsf(__uint_as_float(v.x)), fabsf(__uint_as_float(v.y)), fabsf(__uint_as_float(v.z)),
-                          fabsf(__uint_as_float(v.w))};
+    // queries: 16 rows a warp (32 w + 16 g ..), one a load, a run of lanes
+    {
+      constexpr int LPR = D / 4, RPL = 32 / LPR;
+      const int lane = tid & 31, part = lane % LPR;
+      uint8_t* dst = sm + M::Q + (part >> 4) * 16384 + 8 * (part & 1);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) mx = fmaxf(mx, x[j] < INFINITY ? x[j] : 0.f);
-    }
-    const int e = row_exponent(mx);
-    const float up = pow2i(14 - e), row_scale = pow2i(e - 14);
-    if (g == 0) {
-      uint8_t* dst = sm + M::Q + row * 128;
-#pragma unroll 2
-      for (int c = 0; c < D / 8; ++c) {
-        uint32_t hi[4], lo[4];
+      for (int q = 0; q < 16 / RPL; ++q) {
+        const int from = 16 * g + RPL * q + lane / LPR, at = (row & 96) + from;
+        const int64_t ro = __shfl_sync(0xffffffffu, off, from);
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (__shfl_sync(0xffffffffu, (int)real, from)) v = ldg_v4(static_cast<const float*>(a.Q) + ro + 4 * part);
+        float x[4] = {__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w)};
+        float mx = 0.f;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint4 v = real ? ldg_v4(src + 8 * c + 4 * k) : make_uint4(0u, 0u, 0u, 0u);
-          const float x0 = __uint_as_float(v.x) * up, x1 = __uint_as_float(v.y) * up;
-          const float x2 = __uint_as_float(v.z) * up, x3 = __uint_as_float(v.w) * up;
-          hi[2 * k] = pack_half2(x0, x1);
-          hi[2 * k + 1] = pack_half2(x2, x3);
-          lo[2 * k] = half2_rest(hi[2 * k], x0, x1);
-          lo[2 * k + 1] = half2_rest(hi[2 * k + 1], x2, x3);
-        }
-        uint8_t* at = dst + (c >> 3) * 16384 + (((c & 7) ^ (row & 7)) << 4);
-        *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(at + M::TILE) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fabsf(x[j]) < INFINITY ? fabsf(x[j]) : 0.f);
+#pragma unroll
+        for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const int e = row_exponent(mx);
+        const float up = pow2i(14 - e);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] *= up;
+        const uint32_t h0 = pack_half2(x[0], x[1]), h1 = pack_half2(x[2], x[3]);
+        uint8_t* to = dst + at * 128 + ((((part >> 1) & 7) ^ (at & 7)) << 4);
+        *reinterpret_cast<uint2*>(to) = make_uint2(h0, h1);
+        *reinterpret_cast<uint2*>(to + M::TILE) = make_uint2(half2_rest(h0, x[0], x[1]), half2_rest(h1, x[2], x[3]));
+        if (part == 0) row_e[at] = e;
       }
       fence_proxy_async_smem();
       mbar_arrive(&q_full);
+      ok = kp_wait(&q_full, 0, DEV_ERR_TIMEOUT_A);                     // every row's exponent
     }
+    const float row_scale = pow2i(row_e[row] - 14);
     const uint32_t S = lanes + S_COL + 128u * g;
     const uint64_t rs2 = pack_f2(row_scale, row_scale);
     float m = -INFINITY, l = 0.f;
@@ -903,7 +919,8 @@ kv4_prefill_f32_kernel(const KvStep s, const AttnArgs a, int head0, int heads_he
     for (int g = 0; g < 2; ++g)
       if (fin_m[g][row] != -INFINITY || fin_l[g][row] != 0.f) sum += fin_l[g][row] * ex2(fin_m[g][row] - sum_m);
     float inv = sum_m == -INFINITY && sum == 0.f ? 0.f : 1.0f / sum;   // a query that sees no key: zeros
-    float* out = static_cast<float*>(a.A) + off;
+    // (through the queries' shared memory, free by now, to runs of lanes)
+    uint8_t* stage = sm + M::Q;
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
       float x[32], none = 0.f;
@@ -911,14 +928,26 @@ kv4_prefill_f32_kernel(const KvStep s, const AttnArgs a, int head0, int heads_he
         tmem_ld32(lanes + SUM + c, reinterpret_cast<uint32_t*>(x));
         kp_loads_done(inv, none);
       }
-      if (real) {
 #pragma unroll
-        for (int q = 0; q < 32; q += 4) {
-          float y[4];
+      for (int q = 0; q < 32; q += 4) {
+        float y[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) y[j] = inv == 0.f ? 0.f : x[q + j] * inv;
-          *reinterpret_cast<float4*>(out + c + q) = make_float4(y[0], y[1], y[2], y[3]);
-        }
+        for (int j = 0; j < 4; ++j) y[j] = inv == 0.f ? 0.f : x[q + j] * inv;
+        *reinterpret_cast<float4*>(stage + row * (D * 4) + ((((c + q) >> 2) ^ (row & 7)) << 4)) =
+            make_float4(y[0], y[1], y[2], y[3]);
+      }
+    }
+    __syncwarp();
+    {
+      constexpr int LPR = D / 4, RPL = 32 / LPR;
+      const int lane = tid & 31, part = lane % LPR;
+#pragma unroll 4
+      for (int q = 0; q < LPR; ++q) {
+        const int from = RPL * q + lane / LPR, at = (row & 96) + from;
+        const int64_t ro = __shfl_sync(0xffffffffu, off, from);
+        if (__shfl_sync(0xffffffffu, (int)real, from))
+          *reinterpret_cast<float4*>(static_cast<float*>(a.A) + ro + 4 * part) =
+              *reinterpret_cast<const float4*>(stage + at * (D * 4) + ((part ^ (at & 7)) << 4));
       }
     }
     tc_fence_before();
