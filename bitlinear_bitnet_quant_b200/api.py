@@ -77,7 +77,11 @@ _SIGNATURES = {
                         [_c_void_p] * 2 + [ctypes.c_int, _c_void_p]),
     "bitnet_kv4_attention": (ctypes.c_int, [_c_void_p, ctypes.c_int] + [_c_void_p] * 4 + [_i64] * 3 + [_c_void_p] * 2 +
                              [ctypes.c_int] * 3 + [_i64] * 4 + [_c_void_p] * 2 + [ctypes.c_size_t, _c_void_p]),
-    "bitnet_kv4_attention_workspace_size": (ctypes.c_size_t, [ctypes.c_int] + [_i64] * 2 + [ctypes.c_int] * 3 + [_i64] * 4),
+    "bitnet_kv4_attention_kernel": (ctypes.c_int, [_c_void_p, ctypes.c_int] + [_c_void_p] * 4 + [_i64] * 3 +
+                                    [_c_void_p] * 2 + [ctypes.c_int] * 3 + [_i64] * 4 + [_c_void_p] * 2 +
+                                    [ctypes.c_size_t, ctypes.c_int, _c_void_p]),
+    "bitnet_kv4_attention_workspace_size": (ctypes.c_size_t, [ctypes.c_int] + [_i64] * 2 + [ctypes.c_int] * 3 + [_i64] * 4 +
+                                            [ctypes.c_int]),
     "bitnet_device_error": (ctypes.c_int, [ctypes.POINTER(ctypes.c_int)]),
     "bitnet_measure_i8_mma": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, _c_void_p, _c_void_p,
                                              _c_void_p]),
@@ -531,22 +535,23 @@ def bitnet_kv4_read(cache: KV4Cache, B: int, L: int, t0: int, pos=None, lens=Non
 
 
 def bitnet_kv4_attention_workspace_size(dtype, B: int, L: int, heads: int, kv_heads: int, head_dim: int, T_cap: int,
-                                        window: int = 0, sinks: int = 0, t_max: int = 0) -> int:
-    """Bytes of workspace bitnet_kv4_attention needs for these arguments (0 for few queries)."""
+                                        window: int = 0, sinks: int = 0, t_max: int = 0, kernel: int = 0) -> int:
+    """Bytes of workspace bitnet_kv4_attention needs for these arguments (0: none)."""
     code = {torch.float32: BITNET_F32, torch.bfloat16: BITNET_BF16}[dtype]
     return int(lib().bitnet_kv4_attention_workspace_size(code, B, L, heads, kv_heads, head_dim, T_cap, window, sinks,
-                                                         t_max))
+                                                         t_max, kernel))
 
 
 def bitnet_kv4_attention(Q: torch.Tensor, cache: KV4Cache, B: int, L: int, t0: int, heads: int, window: int = 0,
                          sinks: int = 0, t_max: int | None = None, pos=None, lens=None, A=None, workspace=None,
-                         stream=None):
+                         stream=None, kernel: int = 0):
     """Causal softmax attention of the rows Q [B*L, heads*d] (fp32 or bf16) over a
     4-bit cache; with window > 0 over the last `window` keys and the first `sinks`.
     t_max: a bound on the positions in use plus one (default: t0 + L without pos, else
     T_cap); a query past it counts as outside the cache.  workspace: uint8 scratch of
     bitnet_kv4_attention_workspace_size bytes (allocated here by default).  Returns A in
-    Q's type; rows of padding are left as they were (zeros where A is allocated here)."""
+    Q's type; rows of padding are left as they were (zeros where A is allocated here).
+    kernel != 0 picks the kernels for this call (bitnet_kv4_attention_kernel)."""
     dev = Q.device
     if not Q.is_cuda:
         raise ValueError("Q must be a contiguous CUDA tensor")
@@ -559,14 +564,15 @@ def bitnet_kv4_attention(Q: torch.Tensor, cache: KV4Cache, B: int, L: int, t0: i
     args = (_expect(Q, "Q", Q.dtype, shape, dev), code, *held, B, L, t0,
             _optional(pos, "pos", torch.int32, (B,), dev), _optional(lens, "lens", torch.int32, (B,), dev), heads, kv, d,
             T, window, sinks, t_max, _expect(A, "A", Q.dtype, shape, dev))
+    fn, last = ("bitnet_kv4_attention_kernel", (kernel,)) if kernel else ("bitnet_kv4_attention", ())
     if workspace is not None:
         scratch = (_expect(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.numel())
-        _call("bitnet_kv4_attention", dev, stream, args + scratch)
-    elif _call("bitnet_kv4_attention", dev, stream, args + (None, 0), allowed=_STATUS_WORKSPACE):
-        # many queries: nothing was enqueued yet
-        need = bitnet_kv4_attention_workspace_size(Q.dtype, B, L, heads, kv, d, T, window, sinks, t_max)
+        _call(fn, dev, stream, args + scratch + last)
+    elif _call(fn, dev, stream, args + (None, 0) + last, allowed=_STATUS_WORKSPACE):
+        # a workspace is needed: nothing was enqueued yet
+        need = bitnet_kv4_attention_workspace_size(Q.dtype, B, L, heads, kv, d, T, window, sinks, t_max, kernel)
         workspace = _empty((need,), torch.uint8, dev, stream)
-        _call("bitnet_kv4_attention", dev, stream, args + (workspace.data_ptr(), need))
+        _call(fn, dev, stream, args + (workspace.data_ptr(), need) + last)
     return A
 
 

@@ -51,7 +51,8 @@ bool kv4_prefill_applies(const KvStep& s, const AttnArgs& a, int bf16);
 size_t kv4_prefill_workspace(const KvStep& s, const AttnArgs& a, int bf16, int d);
 cudaError_t run_kv4_prefill(const KvStep& s, const AttnArgs& a, int bf16, int d, void* ws, size_t ws_bytes,
                             cudaStream_t st);
-cudaError_t run_kv4_decode(const KvStep& s, const AttnArgs& a, int bf16, int d, cudaStream_t st);
+size_t kv4_decode_workspace(const KvStep& s, const AttnArgs& a, int d);
+cudaError_t run_kv4_decode(const KvStep& s, const AttnArgs& a, int bf16, int d, void* ws, cudaStream_t st);
 }  // namespace bitnet
 
 namespace {
@@ -552,22 +553,35 @@ static bitnet::AttnArgs kv4_attention_args(int heads, int kv_heads, int64_t wind
   return a;
 }
 
+// kernel: 0 = automatic, 1 = the kernel for few queries, 2 = the one for many (with the expansion)
+static bool kv4_many_queries(const bitnet::KvStep& s, const bitnet::AttnArgs& a, int dtype, int kernel) {
+  return kernel == 2 || (kernel == 0 && bitnet::kv4_prefill_applies(s, a, dtype == BITNET_BF16));
+}
+
+static size_t kv4_workspace(const bitnet::KvStep& s, const bitnet::AttnArgs& a, int dtype, int head_dim, int kernel) {
+  return kv4_many_queries(s, a, dtype, kernel)
+             ? bitnet::kv4_prefill_workspace(s, a, dtype == BITNET_BF16, head_dim)
+             : bitnet::kv4_decode_workspace(s, a, head_dim);
+}
+
 size_t bitnet_kv4_attention_workspace_size(int dtype, int64_t B, int64_t L, int heads, int kv_heads, int head_dim,
-                                           int64_t T_cap, int64_t window, int64_t sinks, int64_t t_max) {
+                                           int64_t T_cap, int64_t window, int64_t sinks, int64_t t_max, int kernel) {
+  if (kernel < 0 || kernel > 2) return 0;
   const int32_t any = 0;                                  // positions may come from the device
   if (kv4_attention_shape(dtype, B, L, 0, &any, heads, kv_heads, head_dim, T_cap, window, sinks, t_max) != BITNET_OK)
     return 0;
   bitnet::KvStep s = kv_step(B, L, 0, nullptr, nullptr, T_cap);
   if (t_max > 0) s.limit = (int)t_max;
   const bitnet::AttnArgs a = kv4_attention_args(heads, kv_heads, window, sinks);
-  if (B == 0 || L == 0 || !bitnet::kv4_prefill_applies(s, a, dtype == BITNET_BF16)) return 0;
-  return bitnet::kv4_prefill_workspace(s, a, dtype == BITNET_BF16, head_dim);
+  return B == 0 || L == 0 ? 0 : kv4_workspace(s, a, dtype, head_dim, kernel);
 }
 
-int bitnet_kv4_attention(const void* Q, int dtype, const uint8_t* Kc, const float* Ks, const uint8_t* Vc,
-                         const float* Vs, int64_t B, int64_t L, int64_t t0, const int32_t* pos, const int32_t* len,
-                         int heads, int kv_heads, int head_dim, int64_t T_cap, int64_t window, int64_t sinks,
-                         int64_t t_max, void* A, void* workspace, size_t workspace_bytes, void* stream) {
+int bitnet_kv4_attention_kernel(const void* Q, int dtype, const uint8_t* Kc, const float* Ks, const uint8_t* Vc,
+                                const float* Vs, int64_t B, int64_t L, int64_t t0, const int32_t* pos,
+                                const int32_t* len, int heads, int kv_heads, int head_dim, int64_t T_cap,
+                                int64_t window, int64_t sinks, int64_t t_max, void* A, void* workspace,
+                                size_t workspace_bytes, int kernel, void* stream) {
+  if (kernel < 0 || kernel > 2) return BITNET_ERR_SHAPE;
   const int sh = kv4_attention_shape(dtype, B, L, t0, pos, heads, kv_heads, head_dim, T_cap, window, sinks, t_max);
   if (sh != BITNET_OK) return sh;
   if (B == 0 || L == 0) return BITNET_OK;
@@ -584,14 +598,23 @@ int bitnet_kv4_attention(const void* Q, int dtype, const uint8_t* Kc, const floa
   a.Vc = Vc;
   a.Vs = Vs;
   a.A = A;
-  const bool prefill = bitnet::kv4_prefill_applies(s, a, dtype == BITNET_BF16);
-  if (prefill && (!workspace || workspace_bytes < bitnet::kv4_prefill_workspace(s, a, dtype == BITNET_BF16, head_dim)))
-    return BITNET_ERR_WORKSPACE;
+  const size_t need = kv4_workspace(s, a, dtype, head_dim, kernel);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return BITNET_ERR_WORKSPACE;
   const int d = check_device();
   if (d != BITNET_OK) return d;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return cuda_status(prefill ? bitnet::run_kv4_prefill(s, a, dtype == BITNET_BF16, head_dim, workspace, workspace_bytes, st)
-                             : bitnet::run_kv4_decode(s, a, dtype == BITNET_BF16, head_dim, st));
+  return cuda_status(
+      kv4_many_queries(s, a, dtype, kernel)
+          ? bitnet::run_kv4_prefill(s, a, dtype == BITNET_BF16, head_dim, workspace, workspace_bytes, st)
+          : bitnet::run_kv4_decode(s, a, dtype == BITNET_BF16, head_dim, workspace, st));
+}
+
+int bitnet_kv4_attention(const void* Q, int dtype, const uint8_t* Kc, const float* Ks, const uint8_t* Vc,
+                         const float* Vs, int64_t B, int64_t L, int64_t t0, const int32_t* pos, const int32_t* len,
+                         int heads, int kv_heads, int head_dim, int64_t T_cap, int64_t window, int64_t sinks,
+                         int64_t t_max, void* A, void* workspace, size_t workspace_bytes, void* stream) {
+  return bitnet_kv4_attention_kernel(Q, dtype, Kc, Ks, Vc, Vs, B, L, t0, pos, len, heads, kv_heads, head_dim, T_cap,
+                                     window, sinks, t_max, A, workspace, workspace_bytes, 0, stream);
 }
 
 int bitnet_device_error(int* code_out) {

@@ -28,7 +28,8 @@ namespace bitnet {
 // head, times a few tokens) cost one product.  A warp takes every (warps)-th tile
 // of 32 keys through its own ring of asynchronous copies; scores, weights and the
 // output stay in its registers.  The warps' partial softmaxes are merged in shared
-// memory, the blocks of a cluster over distributed shared memory.
+// memory; where several blocks share a row tile's keys, over distributed shared memory of
+// a cluster, or (many blocks a row tile) through the workspace by a second kernel.
 // ---------------------------------------------------------------------------
 constexpr int KD_WARPS = 4;
 constexpr int KD_STAGES = 3;
@@ -90,7 +91,7 @@ BN_DEV void kd_stage(const uint8_t* kc, const float* ks, const uint8_t* vc, cons
 
 template <int D, int NT, typename XT>
 __global__ void __launch_bounds__(32 * KD_WARPS, NT == 1 && sizeof(XT) == 2 ? 4 : 1)
-kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e) {
+kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e, int splits, float* parts) {
   constexpr bool SPLIT = sizeof(XT) == 4;            // fp32: two fp16 terms for q and for the weights
   constexpr int ROWS = 8 * NT;
   constexpr int KW = D / 32, VW = D / 64;            // words of a key row, of a value row, a lane holds
@@ -103,9 +104,8 @@ kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e) {
   pdl_launch_dependents();
   pdl_wait();                                        // q and the cache come from the previous kernel
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  uint32_t csize, crank;
-  asm volatile("mov.u32 %0, %cluster_nctaid.x;" : "=r"(csize));
-  asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(crank));
+  // block crank of the csize that share a row tile: of a cluster, or with parts of the grid
+  const uint32_t csize = (uint32_t)splits, crank = blockIdx.x % csize;
   const int group = a.heads / a.kv_heads;
   const int b = blockIdx.z, h = blockIdx.y;
   const int r0 = (int)(blockIdx.x / csize) * ROWS;   // first row (token * group + head of the group)
@@ -429,6 +429,18 @@ kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e) {
     }
     *reinterpret_cast<float4*>(c_o + 4 * e) = acc;
   }
+  if (parts != nullptr) {
+    // this block's state: ROWS maxima, ROWS sums, ROWS outputs
+    __syncthreads();
+    float* out = parts + ((((int64_t)b * a.kv_heads + h) * gridDim.x + blockIdx.x) * (ROWS * (D + 2)));
+    if (tid < ROWS) {
+      out[tid] = c_m[tid];
+      out[ROWS + tid] = c_l[tid];
+    }
+    for (int e = tid; e < ROWS * D / 4; e += 32 * KD_WARPS)
+      *reinterpret_cast<float4*>(out + 2 * ROWS + 4 * e) = *reinterpret_cast<const float4*>(c_o + 4 * e);
+    return;
+  }
   // ---- merged over the cluster: each block takes a share of the outputs ----
   cluster_arrive();
   cluster_wait();
@@ -459,41 +471,129 @@ kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e) {
   cluster_wait();                                    // no block leaves while another reads its shared memory
 }
 
+// The second kernel merges the parts, a block a row: the parts' weights first, then the
+// outputs, two dimensions a thread, the parts shared between 512 / D groups of threads
+// and the groups' sums added in their order.
+constexpr int KD_MAX_SPLITS = 3 * 148;
+template <int D, int ROWS, typename XT>
+__global__ void __launch_bounds__(256)
+kv4_merge_kernel(const KvStep s, const AttnArgs a, int splits, const float* parts) {
+  constexpr int PAIRS = D / 2, GROUPS = 256 / PAIRS, PART = ROWS * (D + 2);
+  __shared__ float w_part[KD_MAX_SPLITS], l_part[KD_MAX_SPLITS];
+  __shared__ float2 x_part[GROUPS][PAIRS];
+  pdl_launch_dependents();
+  pdl_wait();                                        // the parts come from the previous kernel
+  const int group = a.heads / a.kv_heads, b = blockIdx.z, h = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
+  const int tile = blockIdx.x / ROWS, row = blockIdx.x % ROWS, R = tile * ROWS + row;
+  if (R >= kv_real_tokens(s, b) * group) return;
+  const float* p = parts + (((int64_t)b * a.kv_heads + h) * (gridDim.x / ROWS) + tile) * splits * PART;
+  for (int c = tid; c < splits; c += 256) {
+    w_part[c] = p[(int64_t)c * PART + row];
+    l_part[c] = p[(int64_t)c * PART + ROWS + row];
+  }
+  __syncthreads();
+  float mx = -INFINITY;
+  for (int c = lane; c < splits; c += 32) mx = fmaxf(mx, w_part[c]);
+  mx = warp_max(mx);
+  __syncthreads();
+  for (int c = tid; c < splits; c += 256)
+    w_part[c] = w_part[c] == -INFINITY && l_part[c] == 0.f ? 0.f : ex2(w_part[c] - mx);
+  __syncthreads();
+  const int g = tid / PAIRS, pair = tid % PAIRS;
+  float2 x = make_float2(0.f, 0.f);
+#pragma unroll 8
+  for (int c = g; c < splits; c += GROUPS) {
+    const float2 v = *reinterpret_cast<const float2*>(p + (int64_t)c * PART + 2 * ROWS + row * D + 2 * pair);
+    x.x += w_part[c] * v.x;
+    x.y += w_part[c] * v.y;
+  }
+  x_part[g][pair] = x;
+  __syncthreads();
+  if (g != 0) return;
+  float sum = 0.f;
+  for (int c = 0; c < splits; ++c) sum += w_part[c] * l_part[c];
+#pragma unroll
+  for (int i = 1; i < GROUPS; ++i) {
+    x.x += x_part[i][pair].x;
+    x.y += x_part[i][pair].y;
+  }
+  const float r = mx == -INFINITY && sum == 0.f ? 0.f : 1.0f / sum;        // a query that sees no key: zeros
+  const int tok = R / group;
+  const int64_t off = (((int64_t)b * s.L + tok) * a.heads + h * group + R - tok * group) * D + 2 * pair;
+  if constexpr (sizeof(XT) == 4) {
+    *reinterpret_cast<float2*>(static_cast<float*>(a.A) + off) = make_float2(x.x * r, x.y * r);
+  } else {
+    *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(a.A) + off) = __floats2bfloat162_rn(x.x * r, x.y * r);
+  }
+}
+
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-template <int D, int NT, typename XT>
-static cudaError_t launch_decode(const KvStep& s, const AttnArgs& a, int64_t t_max, cudaStream_t st) {
-  constexpr int ROWS = 8 * NT;
-  auto kern = kv4_decode_kernel<D, NT, XT>;
-  const size_t smem = (size_t)KD_WARPS * KD_STAGES * KdTile<D>::BYTES + (size_t)ROWS * D * 4;
-  const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), smem);
-  if (e != cudaSuccess) return e;
-  const int64_t row_tiles = ((int64_t)s.L * (a.heads / a.kv_heads) + ROWS - 1) / ROWS;
-  // a cluster splits the keys of one row tile: until the blocks fill the GPU (three to an
-  // SM) with two tiles a warp at least, and, as sequences may be of very different lengths,
-  // until no warp has more than 16 tiles.  (16 sequences of 2048 to 32768 keys, 8 key heads:
-  // two blocks a cluster 179 us, eight XXX us.)
-  const int64_t blocks = row_tiles * a.kv_heads * s.B;
-  int64_t keys = t_max;
+// How a step's row tiles are split over blocks.
+struct KdSplit {
+  int rows;                                          // a tile
+  int64_t row_tiles;
+  int splits;                                        // blocks a row tile
+  bool parts;                                        // merged through the workspace (else in a cluster)
+};
+static KdSplit kd_split(const KvStep& s, const AttnArgs& a) {
+  KdSplit d;
+  const int64_t rows = (int64_t)s.L * (a.heads / a.kv_heads);
+  d.rows = rows <= 8 ? 8 : 16;
+  d.row_tiles = (rows + d.rows - 1) / d.rows;
+  const int64_t blocks = d.row_tiles * a.kv_heads * s.B;
+  int64_t keys = s.limit;
   if (a.window > 0 && (int64_t)a.window + a.sinks + s.L < keys) keys = (int64_t)a.window + a.sinks + s.L;
   const int64_t per_tile = KD_WARPS * KD_KT;         // keys a block takes with one tile a warp
-  unsigned c = 1;
-  while (c < 8 && ((blocks * c * 2 <= 3 * 148 && keys > c * per_tile * 2) || keys > c * per_tile * 16)) c *= 2;
-  return launch_pdl(kern, dim3((unsigned)(row_tiles * c), (unsigned)a.kv_heads, (unsigned)s.B), dim3(32 * KD_WARPS),
-                    smem, st, dim3(c, 1, 1), s, a, (float)(1.4426950408889634 / sqrt((double)D)));
+  // Few row tiles with long contexts: three blocks to an SM, of two tiles a warp at least, merged by a
+  // second kernel.  (One sequence of 32000 keys, 16 key heads, bf16: clusters of 8 58 us, so SPLIT16 us.)
+  const int64_t fill = KD_MAX_SPLITS / blocks, most = keys / (2 * per_tile);
+  const int64_t n = fill < most ? fill : most;
+  d.parts = n > 8;
+  d.splits = (int)n;
+  if (d.parts) return d;
+  // A cluster: until the blocks fill the GPU (three to an SM) with two tiles a warp at least, and, as
+  // sequences may be of very different lengths, until no warp has more than 16 tiles.  (16 sequences of
+  // 2048 to 32768 keys, 8 key heads: two blocks a cluster 179 us, four 133, eight 117, sixteen 123.)
+  d.splits = 1;
+  while (d.splits < 8 && ((blocks * d.splits * 2 <= 3 * 148 && keys > d.splits * per_tile * 2) ||
+                          keys > d.splits * per_tile * 16))
+    d.splits *= 2;
+  return d;
+}
+// Bytes of the parts (0: none).
+size_t kv4_decode_workspace(const KvStep& s, const AttnArgs& a, int d) {
+  const KdSplit k = kd_split(s, a);
+  return k.parts ? (size_t)(k.row_tiles * a.kv_heads * s.B * k.splits * k.rows * (d + 2)) * sizeof(float) : 0;
+}
+
+template <int D, int NT, typename XT>
+static cudaError_t launch_decode(const KvStep& s, const AttnArgs& a, const KdSplit& k, void* ws, cudaStream_t st) {
+  auto kern = kv4_decode_kernel<D, NT, XT>;
+  const size_t smem = (size_t)KD_WARPS * KD_STAGES * KdTile<D>::BYTES + (size_t)8 * NT * D * 4;
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), smem);
+  if (e != cudaSuccess) return e;
+  float* parts = k.parts ? static_cast<float*>(ws) : nullptr;
+  const unsigned cluster = k.parts ? 1u : (unsigned)k.splits;
+  e = launch_pdl(kern, dim3((unsigned)(k.row_tiles * k.splits), (unsigned)a.kv_heads, (unsigned)s.B),
+                 dim3(32 * KD_WARPS), smem, st, dim3(cluster, 1, 1), s, a,
+                 (float)(1.4426950408889634 / sqrt((double)D)), k.splits, parts);
+  if (e != cudaSuccess || !k.parts) return e;
+  return launch_pdl(kv4_merge_kernel<D, 8 * NT, XT>, dim3((unsigned)(k.row_tiles * 8 * NT), (unsigned)a.kv_heads, (unsigned)s.B),
+                    dim3(256), 0, st, 1u, s, a, k.splits, (const float*)parts);
 }
 
 template <int D, typename XT>
-static cudaError_t launch_attention(const KvStep& s, const AttnArgs& a, cudaStream_t st) {
-  if ((int64_t)s.L * (a.heads / a.kv_heads) <= 8) return launch_decode<D, 1, XT>(s, a, s.limit, st);
-  return launch_decode<D, 2, XT>(s, a, s.limit, st);
+static cudaError_t launch_attention(const KvStep& s, const AttnArgs& a, void* ws, cudaStream_t st) {
+  const KdSplit k = kd_split(s, a);
+  return k.rows == 8 ? launch_decode<D, 1, XT>(s, a, k, ws, st) : launch_decode<D, 2, XT>(s, a, k, ws, st);
 }
 
-cudaError_t run_kv4_decode(const KvStep& s, const AttnArgs& a, int bf16, int d, cudaStream_t st) {
+cudaError_t run_kv4_decode(const KvStep& s, const AttnArgs& a, int bf16, int d, void* ws, cudaStream_t st) {
   using bf = __nv_bfloat16;
-  if (d == 128) return bf16 ? launch_attention<128, bf>(s, a, st) : launch_attention<128, float>(s, a, st);
-  return bf16 ? launch_attention<64, bf>(s, a, st) : launch_attention<64, float>(s, a, st);
+  if (d == 128) return bf16 ? launch_attention<128, bf>(s, a, ws, st) : launch_attention<128, float>(s, a, ws, st);
+  return bf16 ? launch_attention<64, bf>(s, a, ws, st) : launch_attention<64, float>(s, a, ws, st);
 }
 
 }  // namespace bitnet

@@ -303,6 +303,19 @@ BN_DEV void kp_weights(const float (&x)[KP_KT], float f, float ref, uint32_t (&w
   top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
 }
 
+// Masks the scores of N columns: those up to hi, and past lo or below sk, stay.  As bits
+// of words, two instructions a column.
+BN_DEV uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+template <int N>
+BN_DEV void kp_mask(float* x, int hi, int lo, int sk) {
+#pragma unroll
+  for (int c = 0; c < N; c += 32) {
+    const uint32_t seen = bits_below(hi + 1 - c) & (~bits_below(lo + 1 - c) | bits_below(sk - c));
+#pragma unroll
+    for (int q = 0; q < 32; ++q) x[c + q] = (seen >> q) & 1u ? x[c + q] : -INFINITY;
+  }
+}
+
 // Completion of this warp's tensor-memory loads; what their use starts from passes
 // through, so that the compiler keeps every use behind the wait.
 BN_DEV void kp_loads_done(float& ref, float& f) {
@@ -391,7 +404,7 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, int head0, int heads_here, 
       float row_scale;                               // base-2 score of an accumulator, up to the tile's factor
       {
         // the warp's 32 rows, scaled, K-major with 128-byte swizzle.  RPL rows a load, each a run of
-        // lanes: a row a lane took 8000 cycles for its 32 lines a load
+        // lanes
         constexpr int LPR = D / 8, RPL = 32 / LPR;
         const int lane = tid & 31, chunk = lane % LPR;
         uint8_t* dst = sm + M::Q + g * M::TILE + (chunk >> 3) * 16384;
@@ -453,12 +466,7 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, int head0, int heads_here, 
           for (int c = 0; c < 4; ++c) tmem_ld32(S + 32 * c, reinterpret_cast<uint32_t*>(x) + 32 * c);
           float ref = m == -INFINITY ? 0.f : BIAS + F - m;
           kp_loads_done(ref, f);
-          if (!full) {
-            const int hi = p - j0;                                     // columns up to hi, and past lo or below sk
-            const int lo = a.window > 0 ? p - a.window - j0 : -1, sk = a.sinks - j0;
-#pragma unroll
-            for (int c = 0; c < KP_KT; ++c) x[c] = c <= hi && (c > lo || c < sk) ? x[c] : -INFINITY;
-          }
+          if (!full) kp_mask<KP_KT>(x, p - j0, a.window > 0 ? p - a.window - j0 : -1, a.sinks - j0);
           kp_weights(x, f, ref, w, sum, top);
           top = top * f + F;
           if (!__any_sync(0xffffffffu, top > m + MOVE || (m == -INFINITY && top != -INFINITY))) break;
@@ -760,11 +768,7 @@ kv4_prefill_f32_kernel(const KvStep s, const AttnArgs a, int head0, int heads_he
           unpack_f2(fma_f2(pack_f2(x[q], x[q + 1]), mul_f2(kf.x, rs), ef.x), x[q], x[q + 1]);
           unpack_f2(fma_f2(pack_f2(x[q + 2], x[q + 3]), mul_f2(kf.y, rs), ef.y), x[q + 2], x[q + 3]);
         }
-        if (masked) {
-#pragma unroll
-          for (int q = 0; q < 32; ++q)
-            x[q] = 32 * c + q <= hi && (32 * c + q > lo || 32 * c + q < sk) ? x[q] : -INFINITY;
-        }
+        if (masked) kp_mask<32>(x, hi - 32 * c, lo - 32 * c, sk - 32 * c);
       };
       float top = -INFINITY;
 #pragma unroll 1
@@ -1007,10 +1011,28 @@ static cudaError_t launch_prefill(const KvStep& s, const AttnArgs& a, uint8_t* w
   return cudaSuccess;
 }
 
-// Whether the step takes this path (the others need no workspace).
+// Whether the step takes this path, by the time either would take (us, fitted to calls with
+// a cold L2).  Here a block takes 256 (bf16) or 128 (fp32) rows through the keys at 1.75 or
+// 2.2 us a tile behind some 9 us of filling and draining, 148 at a time, after the expansion
+// (80 KB a tile and head); the few-query kernel takes 16 rows a warp-tile of 32 keys, which
+// cost 2.3 or 3.5 ns of the whole GPU, and 22 ns a block.  Measured, this path and the other: bf16, 128 rows of 8
+// heads, 2032 keys 46 and 21; fp32, 128 rows of 16 heads, 2128 keys 58 and 39; 512 causal fp32
+// rows of 16 heads 28 and 34; bf16, 8192 causal tokens of 8 x 4 heads 525 and 3800.
 bool kv4_prefill_applies(const KvStep& s, const AttnArgs& a, int bf16) {
-  (void)bf16;
-  return (int64_t)s.L * (a.heads / a.kv_heads) >= 128;
+  const double rows = (double)s.L * (a.heads / a.kv_heads), heads = (double)a.kv_heads * s.B;
+  double most = s.limit, mean = s.limit - 0.5 * s.L;                   // keys of a row
+  if (mean < 0.5 * s.limit) mean = 0.5 * s.limit;
+  if (a.window > 0) {
+    const double w = (double)a.window + a.sinks;
+    most = w < most ? w : most;
+    mean = w < mean ? w : mean;
+  }
+  const double waves = ceil(rows / (bf16 ? 256.0 : 128.0)) * heads / 148.0;
+  const double tiles = (waves <= 1.0 ? most : mean) / KP_KT + 1.0;
+  const double here = 10.0 + (waves > 1.0 ? waves : 1.0) * ((bf16 ? 1.75 : 2.2) * tiles + 9.0) +
+                      heads * (most / KP_KT + 1.0) * 0.016;
+  const double other = 12.0 + ceil(rows / 16.0) * heads * ((mean / 32.0 + 1.0) * (bf16 ? 2.3e-3 : 3.5e-3) + 0.022);
+  return rows > 16.0 && here < other;
 }
 
 cudaError_t run_kv4_prefill(const KvStep& s, const AttnArgs& a, int bf16, int d, void* ws, size_t ws_bytes,

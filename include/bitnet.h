@@ -413,12 +413,12 @@ BITNET_API int bitnet_kv4_read(const uint8_t* Kc, const float* Ks, const uint8_t
  *          the workspace sized, for it.
  * workspace: device scratch, 16-byte aligned, of at least
  *          bitnet_kv4_attention_workspace_size bytes for the same arguments (0: not
- *          read; steps of few queries need none, others up to 256 MB, or one key head's
- *          share where that is more), overwritten.  Two calls that may run at the same
+ *          read; up to 256 MB, or one key head's share of the cache in fp16 where that
+ *          is more), overwritten.  Two calls that may run at the same
  *          time, captured ones among them, need one each.
- * fp32 softmax; products with fp16 operands that hold the codes exactly, bf16
- * queries to 11 bits and more and fp32 queries to 22 bits, and the weights to 11
- * (bf16) or 22 bits (fp32).
+ * fp32 softmax; products with fp16 operands: fp32 rows against exact codes, queries
+ * and weights to 22 bits; bf16 rows exactly, weights (and, for many queries, code *
+ * step) to 11 bits, steps of 128 keys more than 2^24 apart to fewer.
  */
 BITNET_API int bitnet_kv4_attention(const void* Q, int dtype, const uint8_t* Kc, const float* Ks, const uint8_t* Vc,
                                     const float* Vs, int64_t B, int64_t L, int64_t t0, const int32_t* pos,
@@ -427,7 +427,19 @@ BITNET_API int bitnet_kv4_attention(const void* Q, int dtype, const uint8_t* Kc,
                                     size_t workspace_bytes, void* stream);
 BITNET_API size_t bitnet_kv4_attention_workspace_size(int dtype, int64_t B, int64_t L, int heads, int kv_heads,
                                                       int head_dim, int64_t T_cap, int64_t window, int64_t sinks,
-                                                      int64_t t_max);
+                                                      int64_t t_max, int kernel);
+/*
+ * Diagnostics: bitnet_kv4_attention with the kernels chosen for the call instead of by
+ * the sizes (0 = automatic, 1 = the kernel for few queries, 2 = the kernels for many);
+ * each computes the same attention.  The workspace is the chosen kernels' (the size
+ * function's last argument; 0 for bitnet_kv4_attention).
+ */
+BITNET_API int bitnet_kv4_attention_kernel(const void* Q, int dtype, const uint8_t* Kc, const float* Ks,
+                                           const uint8_t* Vc, const float* Vs, int64_t B, int64_t L, int64_t t0,
+                                           const int32_t* pos, const int32_t* len, int heads, int kv_heads,
+                                           int head_dim, int64_t T_cap, int64_t window, int64_t sinks, int64_t t_max,
+                                           void* A, void* workspace, size_t workspace_bytes, int kernel,
+                                           void* stream);
 
 /*
  * Reads and clears the library's device-side error flag on the current

@@ -90,15 +90,22 @@ def test_read_and_attention_refusals(lib):
     assert rd(K=None, V=None) == 1 and rd(K=BAD) == 3
     assert at(heads=3, kv=2) == 2 and at(w=-1) == 2 and at(s=-1) == 2 and at(tm=65) == 2 and at(tm=-1) == 2
     assert at(Q=None) == 1 and at(A=None) == 1 and at(A=BAD) == 3 and at(ws=BAD) == 3
-    size = lambda dt, L, T=4096, w=0, s=0, tm=0, d=128, B=2: lib.bitnet_kv4_attention_workspace_size(
-        dt, B, L, 8, 2, d, T, w, s, tm)
-    assert size(1, 1) == 0 and size(2, 512) == 0 and size(1, 512, d=32) == 0 and size(1, 512, B=0) == 0
-    need = size(1, 512)
+    size = lambda dt, L, T=4096, w=0, s=0, tm=0, d=128, B=2, k=0: lib.bitnet_kv4_attention_workspace_size(
+        dt, B, L, 8, 2, d, T, w, s, tm, k)
+    assert size(1, 1, T=512) == 0 and size(2, 512) == 0 and size(1, 512, d=32) == 0 and size(1, 512, B=0) == 0
+    assert size(1, 1) == 4 * 16 * 8 * 130 * 4                             # 16 parts of 8 rows, 4 heads
+    need = size(1, 2048)
     assert need == 4 * 32 * (65536 + 16)                                  # 4 heads, 32 tiles of 128 keys
-    assert size(1, 512, tm=1000) == 4 * 8 * (65536 + 16) and size(1, 512, w=100, s=4) == 4 * 7 * (65536 + 16)
-    assert size(1, 512, T=1 << 24) == (1 << 17) * (65536 + 16)            # one head's share
-    assert size(1, 512, B=4096, d=64) <= 256 << 20
-    big = dict(dt=1, B=2, L=512, heads=8, kv=2, T=4096)
+    assert size(0, 2048) == 4 * 32 * (65536 + 2048)
+    assert size(1, 2048, tm=3000) == 4 * 24 * (65536 + 16) and size(1, 2048, w=100, s=4) == 4 * 19 * (65536 + 16)
+    assert size(1, 2048, T=1 << 24) == (1 << 17) * (65536 + 16)           # one head's share
+    assert size(1, 2048, B=4096, d=64) <= 256 << 20
+    assert size(1, 2048, k=1) == 0 and size(1, 1, k=2) == need and size(1, 1, k=3) == 0
+    big = dict(dt=1, B=2, L=2048, heads=8, kv=2, T=4096)
+    a = _rows()
+    for kernel, status in ((3, 2), (-1, 2), (2, 7)):                      # no such kernels; no workspace
+        assert lib.bitnet_kv4_attention_kernel(a["Q"], 0, a["Kc"], a["Ks"], a["Vc"], a["Vs"], 2, 3, 0, None, None, 2, 1,
+                                               128, 64, 0, 0, 0, 0x30000, None, 0, kernel, None) == status
     assert at(**big) == 7 and at(ws=0x50000, wsb=need - 1, **big) == 7
 
 

@@ -266,6 +266,9 @@ ATTENTIONS = [
     (F32, 1, 129, 2047, 2, 2, 128, 1000, 4, None, None),
     (BF16, 1, 1024, 0, 2, 1, 128, 0, 0, None, None),
     (F32, 1, 700, 0, 3, 1, 128, 0, 0, None, None),
+    (F32, 1, 5, 6000, 6, 2, 128, 0, 0, None, None),
+    (BF16, 2, 2, 5000, 8, 2, 64, 3000, 7, "ragged", None),
+    (F32, 1, 1, 3000, 2, 2, 64, 0, 0, None, None),
 ]
 
 
@@ -289,12 +292,14 @@ def _attention_inputs(case, seed=0):
                 lens=ints(new) if lens else None, t0=0 if pos else ctx)
 
 
+@pytest.mark.parametrize("kernel", [0, 1, 2])
 @pytest.mark.parametrize("case", ATTENTIONS)
-def test_kv4_attention(case):
+def test_kv4_attention(case, kernel):
+    """Every case through the kernel for few queries, those for many, and the automatic choice."""
     dtype, B, L, ctx, heads, kv, d, window, sinks, pos, lens = case
     c = _attention_inputs(case)
     A = torch.full((B * L, heads * d), 5.5, dtype=dtype, device="cuda")
-    kw = dict(window=window, sinks=sinks, pos=c["pos"], lens=c["lens"])
+    kw = dict(window=window, sinks=sinks, pos=c["pos"], lens=c["lens"], kernel=kernel)
     out = api.bitnet_kv4_attention(c["q"], c["cache"], B, L, c["t0"], heads, A=A, **kw)
     assert out is A
     got, q = host(A).reshape(B, L, heads, d), c["q64"].reshape(B, L, heads, d)
@@ -310,44 +315,47 @@ def test_kv4_attention(case):
     assert torch.equal(again[real], A[real]) and torch.equal(again[~real], c["q"][~real])
 
 
-def test_kv4_attention_hidden_values_do_not_leak():
+@pytest.mark.parametrize("kernel", [1, 2])
+@pytest.mark.parametrize("L,heads", [(6, 2), (150, 1)])
+def test_kv4_attention_hidden_values_do_not_leak(L, heads, kernel):
     """A query whose tile holds a later token's NaN steps, infinite queries beside it
     and rows outside the cache."""
     rng = np.random.default_rng(11)
-    for L, heads in ((6, 2), (150, 1)):
+    for dtype in (F32, BF16):
         T, d = 160, 128
         cache, k, v = _cache(rng, 1, 1, T, d)
-        q, q64 = rows(rng, L, heads * d, F32)
+        q, q64 = rows(rng, L, heads * d, dtype)
         cache.ks[0, 0, L - 1] = math.nan             # seen by the last token alone
         cache.vs[0, 0, L - 1] = math.nan
         q[2, 0] = math.inf                           # one head row of token 2
         q[3, 1] = math.nan
         q[4] *= 1e30                                 # and a huge row: the others keep their precision
-        A = api.bitnet_kv4_attention(q, cache, 1, L, 0, heads)
+        A = api.bitnet_kv4_attention(q, cache, 1, L, 0, heads, kernel=kernel)
         keep = [l for l in range(L - 1) if l not in (2, 3, 4)]
         got = host(A).reshape(L, heads, d)
         _check_attention(got[keep], q64.reshape(L, heads, d)[keep], np.nan_to_num(k[0]), np.nan_to_num(v[0]),
-                         np.array(keep), heads, 0, 0, False)
+                         np.array(keep), heads, 0, 0, dtype == BF16)
         assert np.isnan(got[L - 1]).all()
         if heads > 1:                                # the other heads of tokens 2 and 3
             for l in (2, 3):
                 _check_attention(got[l:l + 1, 1:], q64.reshape(L, heads, d)[l:l + 1, 1:], k[0], v[0], np.array([l]), 1, 0,
-                                 0, False)
+                                 0, dtype == BF16)
         # a query that sees NaN keys alone
         cache.ks[0, 0, :2] = math.nan
-        A = api.bitnet_kv4_attention(rows(rng, L, heads * d, F32)[0], cache, 1, L, 0, heads)
+        A = api.bitnet_kv4_attention(rows(rng, L, heads * d, dtype)[0], cache, 1, L, 0, heads, kernel=kernel)
         assert A[:2].isnan().all()
         # every position outside the cache: zeros; some outside: those
         for first, zero in ((T, range(L)), (-L, range(L)), (T - 3, range(3, L)), (-2, range(2))):
-            clean = rows(rng, L, heads * d, F32)[0]
+            clean = rows(rng, L, heads * d, dtype)[0]
             A = api.bitnet_kv4_attention(clean, api.KV4Cache(*(torch.nan_to_num(t) if t.is_floating_point() else t
-                                                               for t in cache)), 1, L, 0, heads, pos=ints([first]))
+                                                               for t in cache)), 1, L, 0, heads, pos=ints([first]), kernel=kernel)
             z = (A == 0).all(-1).cpu().numpy()
             assert np.array_equal(np.nonzero(z)[0], np.array(list(zero)))
 
 
+@pytest.mark.parametrize("kernel", [1, 2])
 @pytest.mark.parametrize("dtype", [F32, BF16])
-def test_kv4_attention_wide_steps(dtype):
+def test_kv4_attention_wide_steps(dtype, kernel):
     """Value steps over 40 powers of ten, a zero step among them, and scores that
     grow along the keys: the sum of the weights keeps its keys."""
     rng = np.random.default_rng(5)
@@ -360,12 +368,13 @@ def test_kv4_attention_wide_steps(dtype):
         v = KO.unpack_codes(cache.vc.cpu().numpy()).astype(np.float64) * steps.astype(np.float64)[:, None]
         q, q64 = rows(rng, L, heads * d, dtype, 1.5)
         t0 = T - L
-        A = api.bitnet_kv4_attention(q, cache, 1, L, t0, heads)
+        A = api.bitnet_kv4_attention(q, cache, 1, L, t0, heads, kernel=kernel)
         _check_attention(host(A).reshape(L, heads, d), q64.reshape(L, heads, d), k[0], v[0], t0 + np.arange(L), heads, 0,
                          0, dtype == BF16)
 
 
-def test_zero_steps_keep_their_weight():
+@pytest.mark.parametrize("kernel", [1, 2])
+def test_zero_steps_keep_their_weight(kernel):
     """Keys with a zero value step count in the softmax sum."""
     d, T = 128, 32
     cache = api.bitnet_kv4_cache(1, T, 1, d)         # all codes and steps zero: equal weights
@@ -373,7 +382,7 @@ def test_zero_steps_keep_their_weight():
     cache.vs[0, 0, 7] = 1.0
     for L in (1, 32):
         q = torch.ones((L, d), device="cuda")
-        A = host(api.bitnet_kv4_attention(q, cache, 1, L, T - L, 1))
+        A = host(api.bitnet_kv4_attention(q, cache, 1, L, T - L, 1, kernel=kernel))
         n = T - L + 1 + np.arange(L)
         ref = np.where(n > 7, 1.0 / n, 0.0)[:, None]
         assert np.all(np.abs(A - ref) <= 2.0 ** -20 * ref)
