@@ -406,7 +406,8 @@ def _expect(t: torch.Tensor, name: str, dtype, shape: tuple, device) -> int:
 
 def _row_stride(t: torch.Tensor, name: str, rows: int, width: int, like: torch.Tensor) -> int:
     """Row stride, in values, of t [rows, width] with contiguous rows (a view of a wider tensor is fine)."""
-    if t.shape != (rows, width) or t.stride(1) != 1 or t.dtype != like.dtype or t.device != like.device or not t.is_cuda:
+    if t.shape != (rows, width) or t.stride(1) != 1 or t.dtype != like.dtype or t.device != like.device or \
+            not t.is_cuda:
         if not (t.is_cuda and t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1)):
             raise ValueError(f"{name} must be a CUDA tensor of contiguous rows")
         if t.device != like.device:
@@ -471,7 +472,8 @@ def bitnet_qk_norm_rope_append(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor
     turned queries Qo, fp32 [B*L, heads*d] (pass Q itself, fp32, to turn in place)."""
     kv_heads = heads if kv_heads is None else kv_heads
     dev, rows = Q.device, B * L
-    _require(Kc, "Kc")
+    if not (Kc.is_cuda and Kc.dim() == 3):
+        raise ValueError("Kc must be a CUDA tensor [B, T_cap, kv_heads*d]")
     T, d = Kc.shape[1], Kc.shape[2] // kv_heads
     ldq = _row_stride(Q, "Q", rows, heads * d, Q)
     ldk = _row_stride(K, "K", rows, kv_heads * d, Q)

@@ -380,11 +380,14 @@ cudaError_t run_append(const KvStep& s, const AppendArgs& a, int x_bf16, int d, 
     rope.theta[i] = 2 * i < a.rot_dim ? exp2(-(2.0 * i / a.rot_dim) * log2(base)) : 0.0;
   const bool four = a.Kc4 != nullptr;
   using bf = __nv_bfloat16;
-  if (d == 128)
-    return four ? (x_bf16 ? launch_append<128, bf, true>(s, a, rope, st) : launch_append<128, float, true>(s, a, rope, st))
-                : (x_bf16 ? launch_append<128, bf, false>(s, a, rope, st) : launch_append<128, float, false>(s, a, rope, st));
-  return four ? (x_bf16 ? launch_append<64, bf, true>(s, a, rope, st) : launch_append<64, float, true>(s, a, rope, st))
-              : (x_bf16 ? launch_append<64, bf, false>(s, a, rope, st) : launch_append<64, float, false>(s, a, rope, st));
+  if (d == 128) {
+    if (four && x_bf16) return launch_append<128, bf, true>(s, a, rope, st);
+    if (four) return launch_append<128, float, true>(s, a, rope, st);
+    return x_bf16 ? launch_append<128, bf, false>(s, a, rope, st) : launch_append<128, float, false>(s, a, rope, st);
+  }
+  if (four && x_bf16) return launch_append<64, bf, true>(s, a, rope, st);
+  if (four) return launch_append<64, float, true>(s, a, rope, st);
+  return x_bf16 ? launch_append<64, bf, false>(s, a, rope, st) : launch_append<64, float, false>(s, a, rope, st);
 }
 
 cudaError_t run_kv4_read(const KvStep& s, int kv_heads, int d, const uint8_t* Kc, const float* Ks, const uint8_t* Vc,

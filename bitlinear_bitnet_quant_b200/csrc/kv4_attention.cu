@@ -387,7 +387,7 @@ kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e, int split
   // ---- the warps' states into shared memory, merged over the warps ----
   __syncthreads();                                   // every ring is free
   float* w_o = reinterpret_cast<float*>(kd_smem);    // [KD_WARPS][ROWS][D]
-  static_assert(KD_WARPS * ROWS * D * 4 <= KD_WARPS * KD_STAGES * KdTile<D>::BYTES, "the partial outputs fit the rings");
+  static_assert(ROWS * D * 4 <= KD_STAGES * KdTile<D>::BYTES, "the partial outputs fit the rings");
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -451,7 +451,8 @@ kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e, int split
     for (uint32_t c = 0; c < csize; ++c) mx = fmaxf(mx, ld_cluster_f32(cluster_map(m_a + 4 * row, c)));
     float sum = 0.f, x0 = 0.f, x1 = 0.f;
     for (uint32_t c = 0; c < csize; ++c) {
-      const float mc = ld_cluster_f32(cluster_map(m_a + 4 * row, c)), lc = ld_cluster_f32(cluster_map(l_a + 4 * row, c));
+      const float mc = ld_cluster_f32(cluster_map(m_a + 4 * row, c));
+      const float lc = ld_cluster_f32(cluster_map(l_a + 4 * row, c));
       const float w = mc == -INFINITY && lc == 0.f ? 0.f : ex2(mc - mx);
       sum += w * lc;
       const uint32_t oa = cluster_map(o_a + 4 * (row * D + dim), c);
@@ -464,7 +465,8 @@ kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e, int split
     if constexpr (SPLIT) {
       *reinterpret_cast<float2*>(static_cast<float*>(a.A) + off) = make_float2(x0 * r, x1 * r);
     } else {
-      *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(a.A) + off) = __floats2bfloat162_rn(x0 * r, x1 * r);
+      *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(a.A) + off) =
+          __floats2bfloat162_rn(x0 * r, x1 * r);
     }
   }
   cluster_arrive();
@@ -523,7 +525,8 @@ kv4_merge_kernel(const KvStep s, const AttnArgs a, int splits, const float* part
   if constexpr (sizeof(XT) == 4) {
     *reinterpret_cast<float2*>(static_cast<float*>(a.A) + off) = make_float2(x.x * r, x.y * r);
   } else {
-    *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(a.A) + off) = __floats2bfloat162_rn(x.x * r, x.y * r);
+    *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(a.A) + off) =
+        __floats2bfloat162_rn(x.x * r, x.y * r);
   }
 }
 
@@ -547,7 +550,7 @@ static KdSplit kd_split(const KvStep& s, const AttnArgs& a) {
   if (a.window > 0 && (int64_t)a.window + a.sinks + s.L < keys) keys = (int64_t)a.window + a.sinks + s.L;
   const int64_t per_tile = KD_WARPS * KD_KT;         // keys a block takes with one tile a warp
   // Few row tiles with long contexts: three blocks to an SM, of two tiles a warp at least, merged by a
-  // second kernel.  (One sequence of 32000 keys, 16 key heads, bf16: clusters of 8 58 us, so SPLIT16 us.)
+  // second kernel.  (One sequence of 32000 keys, 16 key heads, bf16: 35 us, in clusters of 8 58 us.)
   const int64_t fill = KD_MAX_SPLITS / blocks, most = keys / (2 * per_tile);
   const int64_t n = fill < most ? fill : most;
   d.parts = n > 8;
@@ -580,8 +583,9 @@ static cudaError_t launch_decode(const KvStep& s, const AttnArgs& a, const KdSpl
                  dim3(32 * KD_WARPS), smem, st, dim3(cluster, 1, 1), s, a,
                  (float)(1.4426950408889634 / sqrt((double)D)), k.splits, parts);
   if (e != cudaSuccess || !k.parts) return e;
-  return launch_pdl(kv4_merge_kernel<D, 8 * NT, XT>, dim3((unsigned)(k.row_tiles * 8 * NT), (unsigned)a.kv_heads, (unsigned)s.B),
-                    dim3(256), 0, st, 1u, s, a, k.splits, (const float*)parts);
+  return launch_pdl(kv4_merge_kernel<D, 8 * NT, XT>,
+                    dim3((unsigned)(k.row_tiles * 8 * NT), (unsigned)a.kv_heads, (unsigned)s.B), dim3(256), 0,
+                    st, 1u, s, a, k.splits, (const float*)parts);
 }
 
 template <int D, typename XT>

@@ -24,7 +24,7 @@ namespace bitnet {
 // 128 keys and 256 rows.
 // ---------------------------------------------------------------------------
 constexpr int KP_KT = 128;                           // keys a tile
-constexpr int KP_POLY = 4;                           // every KP_POLY-th pair's exponentials run on the multiply-add units
+constexpr int KP_POLY = 4;                           // one pair in KP_POLY is raised on the multiply-add units
 // 2^r on [-1/2, 1/2], the cubic of least largest relative error (7.5e-05), by linear programming
 constexpr float EXP2_C0 = 0.999928073f, EXP2_C1 = 0.693260985f, EXP2_C2 = 0.242611125f, EXP2_C3 = 0.055171670f;
 
@@ -125,7 +125,7 @@ kv4_expand_kernel(const KvStep s, const AttnArgs a, int head0, int slots, float 
   const int slot = blockIdx.x;
   if (!seen.any || slot >= tiles.count) return;
   const int j0 = tiles.at(slot) * KP_KT;
-  const int seen_lo = a.window > 0 ? seen.first - a.window : -1;       // keys past it, and the sinks, are seen by some row
+  const int seen_lo = a.window > 0 ? seen.first - a.window : -1;       // some row sees the keys past it, and the sinks
   auto is_seen = [&](int j) { return j <= seen.last && (j > seen_lo || j < a.sinks); };
   // a warp's 32 rows are one run of memory: lane i takes 16 bytes of every D / 2-byte row in turn,
   // part i % PARTS of row i / PARTS + RPI q; step factors come from the lane whose number is the row's
@@ -256,11 +256,13 @@ struct KpRows {
 // 2^x of a pair on the multiply-add units: x = n + r with r in [-1/2, 1/2] by adding
 // 1.5 * 2^23, a cubic for 2^r (relative error 1e-4, a fifth of the fp16 rounding that
 // follows), and n into the exponent.  x below -125 counts as -125 (2^-125 rounds to
-// zero in fp16).
+// zero in fp16); a NaN stays one, through the last sum.
 BN_DEV void exp2_pair(uint64_t x, float& e0, float& e1) {
   float a, b;
   unpack_f2(x, a, b);
-  const uint64_t v = pack_f2(fmaxf(a, -125.f), fmaxf(b, -125.f));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(-125.f));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(b) : "f"(-125.f));
+  const uint64_t v = pack_f2(a, b);
   const uint64_t big = pack_f2(12582912.f, 12582912.f), nbig = pack_f2(-12582912.f, -12582912.f);
   const uint64_t t = add_f2(v, big);
   const uint64_t n = add_f2(t, nbig);
@@ -273,6 +275,7 @@ BN_DEV void exp2_pair(uint64_t x, float& e0, float& e1) {
   unpack_f2(q, q0, q1);
   e0 = __uint_as_float(__float_as_uint(q0) + (__float_as_uint(t0) << 23));
   e1 = __uint_as_float(__float_as_uint(q1) + (__float_as_uint(t1) << 23));
+  unpack_f2(fma_f2(v, 0ull, pack_f2(e0, e1)), e0, e1);
 }
 
 // The weights of a tile's keys for one row, as fp16 pairs, for exponents x f + ref; their
@@ -400,7 +403,8 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, int head0, int heads_here, 
       const int tok = R / group;
       const int64_t off = (((int64_t)b * s.L + tok) * a.heads + h * group + R - tok * group) * D;
       const int64_t pr = p0 + tok;
-      const int p = !real ? rows.p_hi : pr >= 0 && pr < s.limit ? (int)pr : -1;      // padding rows see what their tile does
+      // (a padding row sees what its tile does)
+      const int p = !real ? rows.p_hi : pr >= 0 && pr < s.limit ? (int)pr : -1;
       float row_scale;                               // base-2 score of an accumulator, up to the tile's factor
       {
         // the warp's 32 rows, scaled, K-major with 128-byte swizzle.  RPL rows a load, each a run of
@@ -414,7 +418,8 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, int head0, int heads_here, 
           const int from = RPL * q + lane / LPR;
           const int64_t ro = __shfl_sync(0xffffffffu, off, from);
           v[q] = make_uint4(0u, 0u, 0u, 0u);
-          if (__shfl_sync(0xffffffffu, (int)real, from)) v[q] = ldg_v4(static_cast<const __nv_bfloat16*>(a.Q) + ro + 8 * chunk);
+          if (__shfl_sync(0xffffffffu, (int)real, from))
+            v[q] = ldg_v4(static_cast<const __nv_bfloat16*>(a.Q) + ro + 8 * chunk);
         }
         int my_e = 0;
 #pragma unroll
@@ -434,7 +439,8 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, int head0, int heads_here, 
 #pragma unroll
           for (int j = 0; j < 4; ++j) o[j] = pack_half2(bf16lo(w[j]) * up, bf16hi(w[j]) * up);
           const int at = (row & 96) + RPL * q + lane / LPR;
-          *reinterpret_cast<uint4*>(dst + at * 128 + (((chunk & 7) ^ (at & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(dst + at * 128 + (((chunk & 7) ^ (at & 7)) << 4)) =
+              make_uint4(o[0], o[1], o[2], o[3]);
           const int er = __shfl_sync(0xffffffffu, e, (lane % RPL) * LPR);          // of row RPL q + lane % RPL
           if (lane / RPL == q) my_e = er;
         }
@@ -475,7 +481,7 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, int head0, int heads_here, 
           float down = m == -INFINITY ? 0.f : ex2(m - mn);
           m = mn;
           l *= down;
-          if (used > 0) {                                              // every product so far was issued ahead of these scores
+          if (used > 0) {                            // (every product so far was issued ahead of these scores)
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
               float v[32];
@@ -513,7 +519,8 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, int head0, int heads_here, 
           uint32_t o[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float y0 = inv == 0.f ? 0.f : v[8 * q + 2 * j] * inv, y1 = inv == 0.f ? 0.f : v[8 * q + 2 * j + 1] * inv;
+            const float y0 = inv == 0.f ? 0.f : v[8 * q + 2 * j] * inv;
+            const float y1 = inv == 0.f ? 0.f : v[8 * q + 2 * j + 1] * inv;
             const __nv_bfloat162 hv = __floats2bfloat162_rn(y0, y1);
             o[j] = *reinterpret_cast<const uint32_t*>(&hv);
           }
@@ -531,8 +538,9 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, int head0, int heads_here, 
           const int from = RPL * q + lane / LPR, at = (row & 96) + from;
           const int64_t ro = __shfl_sync(0xffffffffu, off, from);
           if (__shfl_sync(0xffffffffu, (int)(real && ok), from))
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.A) + ro + 8 * chunk) = *reinterpret_cast<const uint4*>(
-                stage + (chunk >> 3) * 16384 + at * 128 + (((chunk & 7) ^ (at & 7)) << 4));
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.A) + ro + 8 * chunk) =
+                *reinterpret_cast<const uint4*>(stage + (chunk >> 3) * 16384 + at * 128 +
+                                                (((chunk & 7) ^ (at & 7)) << 4));
         }
       }
       tc_fence_before();
@@ -557,7 +565,8 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, int head0, int heads_here, 
         // ---------------------------------------------- products
         constexpr uint32_t ID_S = idesc_f16(128, KP_KT, false, false), ID_O = idesc_f16(128, D, false, true);
         bool ok = kp_wait(&q_full, 0, DEV_ERR_TIMEOUT_A);
-        const uint32_t qd = desc_lo(smem_u32(sm + M::Q)), kd = desc_lo(smem_u32(sm + M::K)), vd = desc_lo(smem_u32(sm + M::V));
+        const uint32_t qd = desc_lo(smem_u32(sm + M::Q));
+        const uint32_t kd = desc_lo(smem_u32(sm + M::K)), vd = desc_lo(smem_u32(sm + M::V));
         int used0 = 0, used1 = 0;                    // tiles whose weights were used, by stream
         bool was0 = false, was1 = false;             // the last tile was one of the stream's
         for (int i = 0; i <= tiles.count && ok; ++i) {
@@ -587,7 +596,8 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, int head0, int heads_here, 
               if (now) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                  mma_f16_ss(tmem + S_COL + 128u * g, qd + g * (M::TILE >> 4) + (((k >> 2) * 16384 + (k & 3) * 32) >> 4),
+                  mma_f16_ss(tmem + S_COL + 128u * g,
+                             qd + g * (M::TILE >> 4) + (((k >> 2) * 16384 + (k & 3) * 32) >> 4),
                              kb + (((k >> 2) * 16384 + (k & 3) * 32) >> 4), ID_S, k > 0);
                 mma_commit(&s_full[g]);
               }
@@ -710,7 +720,8 @@ kv4_prefill_f32_kernel(const KvStep s, const AttnArgs a, int head0, int heads_he
     // ------------------------------------------------ scores to weights, one row a thread
     const int g = warp >> 2;
     const int64_t pr = p0 + tok;
-    const int p = !real ? rows.p_hi : pr >= 0 && pr < s.limit ? (int)pr : -1;      // padding rows see what their tile does
+    // (a padding row sees what its tile does)
+    const int p = !real ? rows.p_hi : pr >= 0 && pr < s.limit ? (int)pr : -1;
     // queries: 16 rows a warp (32 w + 16 g ..), one a load, a run of lanes
     {
       constexpr int LPR = D / 4, RPL = 32 / LPR;
@@ -844,9 +855,10 @@ kv4_prefill_f32_kernel(const KvStep s, const AttnArgs a, int head0, int heads_he
     // ------------------------------------------------ products
     constexpr uint32_t ID_S = idesc_f16(128, KP_KT, false, false), ID_O = idesc_f16(128, D, false, true);
     ok = kp_wait(&q_full, 0, DEV_ERR_TIMEOUT_A);
-    const uint32_t qd = desc_lo(smem_u32(sm + M::Q)), kd = desc_lo(smem_u32(sm + M::K)), vd = desc_lo(smem_u32(sm + M::V));
+    const uint32_t qd = desc_lo(smem_u32(sm + M::Q));
+    const uint32_t kd = desc_lo(smem_u32(sm + M::K)), vd = desc_lo(smem_u32(sm + M::V));
     for (int i = 0; i < tiles.count + 2 && ok; ++i) {
-      if (i >= 2) {                                  // the output of tile i - 2, whose weights lie where tile i's scores go
+      if (i >= 2) {                                  // tile i - 2's output: its weights lie where tile i's scores go
         const int t = i - 2;
         ok = kp_wait(&v_full[t & 1], (t >> 1) & 1, DEV_ERR_TIMEOUT_FULL) &&
              kp_wait(&p_full[t & 1], (t >> 1) & 1, DEV_ERR_TIMEOUT_ACC) &&
@@ -877,7 +889,8 @@ kv4_prefill_f32_kernel(const KvStep s, const AttnArgs a, int head0, int heads_he
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
               const uint32_t o = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-              mma_f16_ss(tmem + S_COL + 128u * (i & 1), qd + term * (M::TILE >> 4) + o, kb + o, ID_S, term == 0 || k > 0);
+              mma_f16_ss(tmem + S_COL + 128u * (i & 1), qd + term * (M::TILE >> 4) + o, kb + o, ID_S,
+                         term == 0 || k > 0);
             }
           mma_commit(&s_full[i & 1]);
           mma_commit(&k_empty[i & 1]);

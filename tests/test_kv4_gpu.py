@@ -340,6 +340,14 @@ def test_kv4_attention_hidden_values_do_not_leak(L, heads, kernel):
             for l in (2, 3):
                 _check_attention(got[l:l + 1, 1:], q64.reshape(L, heads, d)[l:l + 1, 1:], k[0], v[0], np.array([l]), 1, 0,
                                  0, dtype == BF16)
+        # a NaN key makes exactly the queries that see it NaN, wherever it lies in its tile
+        for j in (0, 3, 6, 7, 13, 33, 70, 127):
+            if j < L - 1:
+                one, _, _ = _cache(rng, 1, 1, T, d)
+                (one.vs if j % 2 else one.ks)[0, 0, j] = math.nan
+                A = api.bitnet_kv4_attention(rows(rng, L, heads * d, dtype)[0], one, 1, L, 0, heads, kernel=kernel)
+                assert torch.equal(A.isnan().all(-1), torch.arange(L, device="cuda") >= j)
+                assert torch.equal(A.isnan().any(-1), torch.arange(L, device="cuda") >= j)
         # a query that sees NaN keys alone
         cache.ks[0, 0, :2] = math.nan
         A = api.bitnet_kv4_attention(rows(rng, L, heads * d, dtype)[0], cache, 1, L, 0, heads, kernel=kernel)
