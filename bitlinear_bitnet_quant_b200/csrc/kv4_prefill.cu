@@ -462,7 +462,7 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, int head0, int heads_here, 
         if (!ok) break;
         tc_fence_after();
         const float F = st.y;
-        float f = fmaxf(st.x * row_scale, 0x1p-126f);
+        float f = fminf(fmaxf(st.x * row_scale, 0x1p-126f), 0x1p127f);         // finite: 0 f is 0
         const bool full = rows.full(j0, KP_KT, a.window, a.sinks);
         uint32_t w[KP_KT / 2];
         float sum, top;
@@ -475,8 +475,9 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, int head0, int heads_here, 
           if (!full) kp_mask<KP_KT>(x, p - j0, a.window > 0 ? p - a.window - j0 : -1, a.sinks - j0);
           kp_weights(x, f, ref, w, sum, top);
           top = top * f + F;
-          if (!__any_sync(0xffffffffu, top > m + MOVE || (m == -INFINITY && top != -INFINITY))) break;
-          // a row exceeds its maximum by too much (or sees its first key): move the maximum
+          // a row exceeds its maximum by too much (or sees its first key): move the maximum, once.  A row
+          // of NaN scores has no maximum and must not ask for one (no comparison with NaN holds)
+          if (!__any_sync(0xffffffffu, top > m + MOVE || (m == -INFINITY && top > -INFINITY))) break;
           const float mn = fmaxf(m, top);
           float down = m == -INFINITY ? 0.f : ex2(m - mn);
           m = mn;

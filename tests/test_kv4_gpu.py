@@ -363,6 +363,32 @@ def test_kv4_attention_hidden_values_do_not_leak(L, heads, kernel):
 
 @pytest.mark.parametrize("kernel", [1, 2])
 @pytest.mark.parametrize("dtype", [F32, BF16])
+def test_kv4_attention_rows_that_are_not_finite(dtype, kernel):
+    """Queries, and whole blocks of keys, that are not finite make their rows NaN and no others."""
+    rng = np.random.default_rng(23)
+    L, heads, d, T = 300, 2, 64, 304
+    at = np.arange(L)
+    for nan_keys in (False, True):
+        cache, k, v = _cache(rng, 1, 1, T, d)
+        q, q64 = rows(rng, L, heads * d, dtype, 1.5)
+        if nan_keys:                                     # keys 128 .. 255, a whole tile
+            cache.ks[:, :, 128:256] = math.nan
+            bad = at >= 128
+        else:
+            q[5], q[200], q[250, ::d] = math.nan, math.nan, math.inf
+            bad = np.isin(at, (5, 200, 250))
+        A = host(api.bitnet_kv4_attention(q, cache, 1, L, 0, heads, kernel=kernel)).reshape(L, heads, d)
+        assert np.isnan(A[bad]).all()
+        _check_attention(A[~bad], q64.reshape(L, heads, d)[~bad], k[0], v[0], at[~bad], heads, 0, 0, dtype == BF16)
+    # scores past the range of fp32, zeros among them
+    cache.ks.fill_(2.0 ** 59)
+    cache.kc[:, :, ::2] = 0
+    A = api.bitnet_kv4_attention(torch.full_like(q, 1e38), cache, 1, L, 0, heads, kernel=kernel)
+    assert A.shape == q.shape and api.bitnet_device_error() == 0
+
+
+@pytest.mark.parametrize("kernel", [1, 2])
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_kv4_attention_wide_steps(dtype, kernel):
     """Value steps over 40 powers of ten, a zero step among them, and scores that
     grow along the keys: the sum of the weights keeps its keys."""
