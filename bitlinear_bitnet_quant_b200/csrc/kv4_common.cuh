@@ -125,6 +125,11 @@ BN_DEV float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+BN_DEV float max3_nan(float a, float b, float c) {   // NaN where one of them is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 
 // A step's exponent e, at least -24: the append writes steps of 2^-20 and more (or a
 // row is empty, step 0, and keeps its weight in the sum).  Together with steps below

@@ -256,13 +256,11 @@ struct KpRows {
 // 2^x of a pair on the multiply-add units: x = n + r with r in [-1/2, 1/2] by adding
 // 1.5 * 2^23, a cubic for 2^r (relative error 1e-4, a fifth of the fp16 rounding that
 // follows), and n into the exponent.  x below -125 counts as -125 (2^-125 rounds to
-// zero in fp16); a NaN stays one, through the last sum.
+// zero in fp16), and so does NaN: the row's maximum carries it (kp_weights).
 BN_DEV void exp2_pair(uint64_t x, float& e0, float& e1) {
   float a, b;
   unpack_f2(x, a, b);
-  asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(-125.f));
-  asm("max.NaN.f32 %0, %0, %1;" : "+f"(b) : "f"(-125.f));
-  const uint64_t v = pack_f2(a, b);
+  const uint64_t v = pack_f2(fmaxf(a, -125.f), fmaxf(b, -125.f));
   const uint64_t big = pack_f2(12582912.f, 12582912.f), nbig = pack_f2(-12582912.f, -12582912.f);
   const uint64_t t = add_f2(v, big);
   const uint64_t n = add_f2(t, nbig);
@@ -275,7 +273,6 @@ BN_DEV void exp2_pair(uint64_t x, float& e0, float& e1) {
   unpack_f2(q, q0, q1);
   e0 = __uint_as_float(__float_as_uint(q0) + (__float_as_uint(t0) << 23));
   e1 = __uint_as_float(__float_as_uint(q1) + (__float_as_uint(t1) << 23));
-  unpack_f2(fma_f2(v, 0ull, pack_f2(e0, e1)), e0, e1);
 }
 
 // The weights of a tile's keys for one row, as fp16 pairs, for exponents x f + ref; their
@@ -288,7 +285,7 @@ BN_DEV void kp_weights(const float (&x)[KP_KT], float f, float ref, uint32_t (&w
 #pragma unroll
   for (int c = 0; c < KP_KT / 2; ++c) {
     float e0, e1;
-    mx[c & 3] = max3(mx[c & 3], x[2 * c], x[2 * c + 1]);
+    mx[c & 3] = max3_nan(mx[c & 3], x[2 * c], x[2 * c + 1]);
     const uint64_t y = fma_f2(pack_f2(x[2 * c], x[2 * c + 1]), f2, ref2);
     if (c % KP_POLY == KP_POLY - 1) {
       exp2_pair(y, e0, e1);
@@ -302,8 +299,8 @@ BN_DEV void kp_weights(const float (&x)[KP_KT], float f, float ref, uint32_t (&w
   }
   float s0, s1;
   unpack_f2(add_f2(add_f2(s2[0], s2[1]), add_f2(s2[2], s2[3])), s0, s1);
-  sum = s0 + s1;
-  top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+  top = max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]);
+  sum = top != top ? top : s0 + s1;                  // a NaN score makes the row NaN, through its sum
 }
 
 // Masks the scores of N columns: those up to hi, and past lo or below sk, stay.  As bits
