@@ -20,8 +20,8 @@ namespace bitnet {
 // The workspace holds, for every key head and tile, the two operands as the images that
 // shared memory takes (128-byte swizzle), so that a tile is one bulk copy, and c and F.
 // Expanding inside the attention kernel, by eight more warps of each block, cost as
-// many issue slots as the softmax and read the codes once a block: 4200 cycles a tile of
-// 128 keys and 256 rows.
+// many issue slots as the softmax and read the codes once a block: 4096 causal tokens of
+// 8 x 4 heads took 179 us, so 173.
 // ---------------------------------------------------------------------------
 constexpr int KP_KT = 128;                           // keys a tile
 constexpr int KP_POLY = 4;                           // one pair in KP_POLY is raised on the multiply-add units
@@ -203,6 +203,15 @@ kv4_expand_kernel(const KvStep s, const AttnArgs a, int head0, int slots, float 
   }
 }
 
+// Whether a block's rows are all padding; such blocks of a ragged step leave before they take
+// tensor memory, which the next block of their SM would wait for.
+BN_DEV bool kp_padding(const KvStep& s, const AttnArgs& a, int head0, int heads_here, int row_tiles, int rows) {
+  if (s.len == nullptr) return false;
+  pdl_wait();
+  const int rt = row_tiles - 1 - (int)(blockIdx.x / heads_here), here = (int)(blockIdx.x % heads_here);
+  return rt * rows >= kv_real_tokens(s, (head0 + here) / a.kv_heads) * (a.heads / a.kv_heads);
+}
+
 // ---------------------------------------------------------------------------
 // Attention.  A block takes 256 rows (token, head of the group) of one key head as two
 // streams of 128: one warp copies tiles of 128 keys into shared memory (two stages), one
@@ -354,6 +363,7 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, int head0, int heads_here, 
   __shared__ uint32_t tmem_sh;
   uint8_t* sm = smem_align(kp_raw, 1024);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  if (kp_padding(s, a, head0, heads_here, row_tiles, 256)) return;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], 1);
@@ -398,235 +408,233 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, int head0, int heads_here, 
     return (int64_t)here * slots + (j < all.sink_tiles ? j : j - all.first + all.sink_tiles);
   };
 
-  if (r0 < n_rows) {
-    if (warp < 8) {
-      // ------------------------------------------------ a stream: scores to weights, one row a thread
-      const int g = warp >> 2, row = tid & 127;
-      const KpRows& rows = g == 0 ? rows0 : rows1;
-      const int R = r0 + 128 * g + row;
-      const bool real = R < n_rows;
-      const int tok = R / group;
-      const int64_t off = (((int64_t)b * s.L + tok) * a.heads + h * group + R - tok * group) * D;
-      const int64_t pr = p0 + tok;
-      // (a padding row sees what its tile does)
-      const int p = !real ? rows.p_hi : pr >= 0 && pr < s.limit ? (int)pr : -1;
-      float row_scale;                               // base-2 score of an accumulator, up to the tile's factor
-      {
-        // the warp's 32 rows, scaled, K-major with 128-byte swizzle.  RPL rows a load, each a run of
-        // lanes
-        constexpr int LPR = D / 8, RPL = 32 / LPR;
-        const int lane = tid & 31, chunk = lane % LPR;
-        uint8_t* dst = sm + M::Q + g * M::TILE + (chunk >> 3) * 16384;
-        uint4 v[LPR];
+  if (warp < 8) {
+    // ------------------------------------------------ a stream: scores to weights, one row a thread
+    const int g = warp >> 2, row = tid & 127;
+    const KpRows& rows = g == 0 ? rows0 : rows1;
+    const int R = r0 + 128 * g + row;
+    const bool real = R < n_rows;
+    const int tok = R / group;
+    const int64_t off = (((int64_t)b * s.L + tok) * a.heads + h * group + R - tok * group) * D;
+    const int64_t pr = p0 + tok;
+    // (a padding row sees what its tile does)
+    const int p = !real ? rows.p_hi : pr >= 0 && pr < s.limit ? (int)pr : -1;
+    float row_scale;                               // base-2 score of an accumulator, up to the tile's factor
+    {
+      // the warp's 32 rows, scaled, K-major with 128-byte swizzle.  RPL rows a load, each a run of
+      // lanes
+      constexpr int LPR = D / 8, RPL = 32 / LPR;
+      const int lane = tid & 31, chunk = lane % LPR;
+      uint8_t* dst = sm + M::Q + g * M::TILE + (chunk >> 3) * 16384;
+      uint4 v[LPR];
 #pragma unroll
-        for (int q = 0; q < LPR; ++q) {
-          const int from = RPL * q + lane / LPR;
-          const int64_t ro = __shfl_sync(0xffffffffu, off, from);
-          v[q] = make_uint4(0u, 0u, 0u, 0u);
-          if (__shfl_sync(0xffffffffu, (int)real, from))
-            v[q] = ldg_v4(static_cast<const __nv_bfloat16*>(a.Q) + ro + 8 * chunk);
-        }
-        int my_e = 0;
-#pragma unroll
-        for (int q = 0; q < LPR; ++q) {
-          const uint32_t w[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
-          float mx = 0.f;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float lo = fabsf(bf16lo(w[j])), hi = fabsf(bf16hi(w[j]));
-            mx = max3(mx, lo < INFINITY ? lo : 0.f, hi < INFINITY ? hi : 0.f);
-          }
-#pragma unroll
-          for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          const int e = row_exponent(mx);
-          const float up = pow2i(14 - e);
-          uint32_t o[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) o[j] = pack_half2(bf16lo(w[j]) * up, bf16hi(w[j]) * up);
-          const int at = (row & 96) + RPL * q + lane / LPR;
-          *reinterpret_cast<uint4*>(dst + at * 128 + (((chunk & 7) ^ (at & 7)) << 4)) =
-              make_uint4(o[0], o[1], o[2], o[3]);
-          const int er = __shfl_sync(0xffffffffu, e, (lane % RPL) * LPR);          // of row RPL q + lane % RPL
-          if (lane / RPL == q) my_e = er;
-        }
-        row_scale = pow2i(my_e - 14);
-        fence_proxy_async_smem();
-        mbar_arrive(&q_full);
+      for (int q = 0; q < LPR; ++q) {
+        const int from = RPL * q + lane / LPR;
+        const int64_t ro = __shfl_sync(0xffffffffu, off, from);
+        v[q] = make_uint4(0u, 0u, 0u, 0u);
+        if (__shfl_sync(0xffffffffu, (int)real, from))
+          v[q] = ldg_v4(static_cast<const __nv_bfloat16*>(a.Q) + ro + 8 * chunk);
       }
-      const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-      const uint32_t S = lanes + S_COL + 128u * g, O = lanes + O_COL + 128u * g;
-      float m = -INFINITY;
-      float l = 0.f;
-      bool ok = true;
-      int used = 0;                                  // tiles of this stream so far
-      for (int i = 0; i < tiles.count && ok; ++i) {
-        const int j0 = tiles.at(i) * KP_KT;
-        if (!rows.any(j0, KP_KT, a.window, a.sinks)) continue;
-        const float2 st = factors[slot(i)];
-        ok = kp_wait(&s_full[g], used & 1, DEV_ERR_TIMEOUT_ACC);
-        if (!ok) break;
-        tc_fence_after();
-        const float F = st.y;
-        float f = fminf(fmaxf(st.x * row_scale, 0x1p-126f), 0x1p127f);         // finite: 0 f is 0
-        const bool full = rows.full(j0, KP_KT, a.window, a.sinks);
-        uint32_t w[KP_KT / 2];
-        float sum;
-        auto weights = [&](bool find_top) {          // with the maximum m; or the largest score
-          float x[KP_KT], top = 0.f;
+      int my_e = 0;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(S + 32 * c, reinterpret_cast<uint32_t*>(x) + 32 * c);
-          float ref = m == -INFINITY ? 0.f : BIAS + F - m;
-          kp_loads_done(ref, f);
-          if (!full) kp_mask<KP_KT>(x, p - j0, a.window > 0 ? p - a.window - j0 : -1, a.sinks - j0);
-          if (find_top) top = kp_top(x);
-          else kp_weights(x, f, ref, w, sum);
-          return top;
-        };
-        weights(false);
-        // a row that sees its first key, or whose weights may pass fp16: move the maximum
-        const int j1 = p < j0 + KP_KT - 1 ? p : j0 + KP_KT - 1;
-        const bool sees = p >= j0 && (a.window == 0 || j1 > p - a.window || j0 < a.sinks);
-        if (__any_sync(0xffffffffu, !(sum <= 65504.f) || (m == -INFINITY && sees))) {
-          const float top = weights(true) * f + F, mn = top > m ? top : m;
-          float down = m == -INFINITY ? 0.f : ex2(m - mn), none = 0.f;
-          m = mn;
-          l *= down;
-          if (used > 0) {                            // (every product so far was issued ahead of these scores)
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              float v[32];
-              tmem_ld32(O + c, reinterpret_cast<uint32_t*>(v));
-              kp_loads_done(down, none);
+      for (int q = 0; q < LPR; ++q) {
+        const uint32_t w[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
+        float mx = 0.f;
 #pragma unroll
-              for (int q = 0; q < 32; ++q) v[q] *= down;
-              tmem_st32(O + c, reinterpret_cast<uint32_t (&)[32]>(v));
-            }
-          }
-          weights(false);
-          if (!(top < INFINITY)) sum = NAN;          // a row of such scores
+        for (int j = 0; j < 4; ++j) {
+          const float lo = fabsf(bf16lo(w[j])), hi = fabsf(bf16hi(w[j]));
+          mx = max3(mx, lo < INFINITY ? lo : 0.f, hi < INFINITY ? hi : 0.f);
         }
-        tmem_st32(S, *reinterpret_cast<uint32_t (*)[32]>(w));          // over scores that have been read
-        tmem_st32(S + 32, *reinterpret_cast<uint32_t (*)[32]>(w + 32));
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&p_full[g]);
-        l += sum * pow2i(-(int)F);
-        ++used;
+#pragma unroll
+        for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const int e = row_exponent(mx);
+        const float up = pow2i(14 - e);
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = pack_half2(bf16lo(w[j]) * up, bf16hi(w[j]) * up);
+        const int at = (row & 96) + RPL * q + lane / LPR;
+        *reinterpret_cast<uint4*>(dst + at * 128 + (((chunk & 7) ^ (at & 7)) << 4)) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+        const int er = __shfl_sync(0xffffffffu, e, (lane % RPL) * LPR);          // of row RPL q + lane % RPL
+        if (lane / RPL == q) my_e = er;
       }
-      // ---- the output, divided by the sum ----
-      if (ok && used > 0) ok = kp_wait(&all_done, 0, DEV_ERR_TIMEOUT_ACC);
+      row_scale = pow2i(my_e - 14);
+      fence_proxy_async_smem();
+      mbar_arrive(&q_full);
+    }
+    const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t S = lanes + S_COL + 128u * g, O = lanes + O_COL + 128u * g;
+    float m = -INFINITY;
+    float l = 0.f;
+    bool ok = true;
+    int used = 0;                                  // tiles of this stream so far
+    for (int i = 0; i < tiles.count && ok; ++i) {
+      const int j0 = tiles.at(i) * KP_KT;
+      if (!rows.any(j0, KP_KT, a.window, a.sinks)) continue;
+      const float2 st = factors[slot(i)];
+      ok = kp_wait(&s_full[g], used & 1, DEV_ERR_TIMEOUT_ACC);
+      if (!ok) break;
       tc_fence_after();
-      float inv = m == -INFINITY && l == 0.f ? 0.f : 0x1p-11f / l;      // a query that sees no key: zeros
-      // (through the queries' shared memory, free by now, to runs of lanes)
-      uint8_t* stage = sm + M::Q + g * M::TILE;
+      const float F = st.y;
+      float f = fminf(fmaxf(st.x * row_scale, 0x1p-126f), 0x1p127f);         // finite: 0 f is 0
+      const bool full = rows.full(j0, KP_KT, a.window, a.sinks);
+      uint32_t w[KP_KT / 2];
+      float sum;
+      auto weights = [&](bool find_top) {          // with the maximum m; or the largest score
+        float x[KP_KT], top = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(S + 32 * c, reinterpret_cast<uint32_t*>(x) + 32 * c);
+        float ref = m == -INFINITY ? 0.f : BIAS + F - m;
+        kp_loads_done(ref, f);
+        if (!full) kp_mask<KP_KT>(x, p - j0, a.window > 0 ? p - a.window - j0 : -1, a.sinks - j0);
+        if (find_top) top = kp_top(x);
+        else kp_weights(x, f, ref, w, sum);
+        return top;
+      };
+      weights(false);
+      // a row that sees its first key, or whose weights may pass fp16: move the maximum
+      const int j1 = p < j0 + KP_KT - 1 ? p : j0 + KP_KT - 1;
+      const bool sees = p >= j0 && (a.window == 0 || j1 > p - a.window || j0 < a.sinks);
+      if (__any_sync(0xffffffffu, !(sum <= 65504.f) || (m == -INFINITY && sees))) {
+        const float top = weights(true) * f + F, mn = top > m ? top : m;
+        float down = m == -INFINITY ? 0.f : ex2(m - mn), none = 0.f;
+        m = mn;
+        l *= down;
+        if (used > 0) {                            // (every product so far was issued ahead of these scores)
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        float v[32], none = 0.f;
-        if (used > 0) {
-          tmem_ld32(O + c, reinterpret_cast<uint32_t*>(v));
-          kp_loads_done(inv, none);
-        }
+          for (int c = 0; c < D; c += 32) {
+            float v[32];
+            tmem_ld32(O + c, reinterpret_cast<uint32_t*>(v));
+            kp_loads_done(down, none);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t o[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float y0 = inv == 0.f ? 0.f : v[8 * q + 2 * j] * inv;
-            const float y1 = inv == 0.f ? 0.f : v[8 * q + 2 * j + 1] * inv;
-            const __nv_bfloat162 hv = __floats2bfloat162_rn(y0, y1);
-            o[j] = *reinterpret_cast<const uint32_t*>(&hv);
+            for (int q = 0; q < 32; ++q) v[q] *= down;
+            tmem_st32(O + c, reinterpret_cast<uint32_t (&)[32]>(v));
           }
-          const int chunk = c / 8 + q;
-          *reinterpret_cast<uint4*>(stage + (chunk >> 3) * 16384 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)) =
-              make_uint4(o[0], o[1], o[2], o[3]);
         }
+        weights(false);
+        if (!(top < INFINITY)) sum = NAN;          // a row of such scores
       }
-      __syncwarp();
-      {
-        constexpr int LPR = D / 8, RPL = 32 / LPR;
-        const int lane = tid & 31, chunk = lane % LPR;
-#pragma unroll 4
-        for (int q = 0; q < LPR; ++q) {
-          const int from = RPL * q + lane / LPR, at = (row & 96) + from;
-          const int64_t ro = __shfl_sync(0xffffffffu, off, from);
-          if (__shfl_sync(0xffffffffu, (int)(real && ok), from))
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.A) + ro + 8 * chunk) =
-                *reinterpret_cast<const uint4*>(stage + (chunk >> 3) * 16384 + at * 128 +
-                                                (((chunk & 7) ^ (at & 7)) << 4));
-        }
-      }
+      tmem_st32(S, *reinterpret_cast<uint32_t (*)[32]>(w));          // over scores that have been read
+      tmem_st32(S + 32, *reinterpret_cast<uint32_t (*)[32]>(w + 32));
+      tmem_wait_st();
       tc_fence_before();
-    } else if (warp == 9) {
-      // ------------------------------------------------ copies
-      bool ok = true;
-      for (int i = 0; i < tiles.count && ok; ++i) {
-        const uint8_t* src = images + slot(i) * (2 * M::TILE);
+      mbar_arrive(&p_full[g]);
+      l += sum * pow2i(-(int)F);
+      ++used;
+    }
+    // ---- the output, divided by the sum ----
+    if (ok && used > 0) ok = kp_wait(&all_done, 0, DEV_ERR_TIMEOUT_ACC);
+    tc_fence_after();
+    float inv = m == -INFINITY && l == 0.f ? 0.f : 0x1p-11f / l;      // a query that sees no key: zeros
+    // (through the queries' shared memory, free by now, to runs of lanes)
+    uint8_t* stage = sm + M::Q + g * M::TILE;
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+      float v[32], none = 0.f;
+      if (used > 0) {
+        tmem_ld32(O + c, reinterpret_cast<uint32_t*>(v));
+        kp_loads_done(inv, none);
+      }
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          uint64_t *full = v ? &v_full[i & 1] : &k_full[i & 1], *empty = v ? &v_empty[i & 1] : &k_empty[i & 1];
-          if (i >= 2 && ok) ok = kp_wait(empty, ((i >> 1) - 1) & 1, DEV_ERR_TIMEOUT_EMPTY);
-          if (ok && elect_one()) {
-            mbar_arrive_expect_tx(full, M::TILE);
-            bulk_load(sm + (v ? M::V : M::K) + (i & 1) * M::TILE, src + v * M::TILE, M::TILE, full);
+      for (int q = 0; q < 4; ++q) {
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float y0 = inv == 0.f ? 0.f : v[8 * q + 2 * j] * inv;
+          const float y1 = inv == 0.f ? 0.f : v[8 * q + 2 * j + 1] * inv;
+          const __nv_bfloat162 hv = __floats2bfloat162_rn(y0, y1);
+          o[j] = *reinterpret_cast<const uint32_t*>(&hv);
+        }
+        const int chunk = c / 8 + q;
+        *reinterpret_cast<uint4*>(stage + (chunk >> 3) * 16384 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+    __syncwarp();
+    {
+      constexpr int LPR = D / 8, RPL = 32 / LPR;
+      const int lane = tid & 31, chunk = lane % LPR;
+#pragma unroll 4
+      for (int q = 0; q < LPR; ++q) {
+        const int from = RPL * q + lane / LPR, at = (row & 96) + from;
+        const int64_t ro = __shfl_sync(0xffffffffu, off, from);
+        if (__shfl_sync(0xffffffffu, (int)(real && ok), from))
+          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.A) + ro + 8 * chunk) =
+              *reinterpret_cast<const uint4*>(stage + (chunk >> 3) * 16384 + at * 128 +
+                                              (((chunk & 7) ^ (at & 7)) << 4));
+      }
+    }
+    tc_fence_before();
+  } else if (warp == 9) {
+    // ------------------------------------------------ copies
+    bool ok = true;
+    for (int i = 0; i < tiles.count && ok; ++i) {
+      const uint8_t* src = images + slot(i) * (2 * M::TILE);
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        uint64_t *full = v ? &v_full[i & 1] : &k_full[i & 1], *empty = v ? &v_empty[i & 1] : &k_empty[i & 1];
+        if (i >= 2 && ok) ok = kp_wait(empty, ((i >> 1) - 1) & 1, DEV_ERR_TIMEOUT_EMPTY);
+        if (ok && elect_one()) {
+          mbar_arrive_expect_tx(full, M::TILE);
+          bulk_load(sm + (v ? M::V : M::K) + (i & 1) * M::TILE, src + v * M::TILE, M::TILE, full);
+        }
+        __syncwarp();
+      }
+    }
+  } else {
+    if (warp == 8 && tiles.count > 0) {
+      // ---------------------------------------------- products
+      constexpr uint32_t ID_S = idesc_f16(128, KP_KT, false, false), ID_O = idesc_f16(128, D, false, true);
+      bool ok = kp_wait(&q_full, 0, DEV_ERR_TIMEOUT_A);
+      const uint32_t qd = desc_lo(smem_u32(sm + M::Q));
+      const uint32_t kd = desc_lo(smem_u32(sm + M::K)), vd = desc_lo(smem_u32(sm + M::V));
+      int used0 = 0, used1 = 0;                    // tiles whose weights were used, by stream
+      bool was0 = false, was1 = false;             // the last tile was one of the stream's
+      for (int i = 0; i <= tiles.count && ok; ++i) {
+        const bool more = i < tiles.count;
+        const int j0 = more ? tiles.at(i) * KP_KT : 0;
+        const bool now0 = more && rows0.any(j0, KP_KT, a.window, a.sinks);
+        const bool now1 = more && rows1.any(j0, KP_KT, a.window, a.sinks);
+        const uint32_t kb = kd + (i & 1) * (M::TILE >> 4), vb = vd + ((i - 1) & 1) * (M::TILE >> 4);
+        // every wait costs some 200 cycles here, also for what is long there: the copies' ones first,
+        // while the weights are still being computed
+        if (more) ok = kp_wait(&k_full[i & 1], (i >> 1) & 1, DEV_ERR_TIMEOUT_FULL);
+        if (i > 0 && ok) ok = kp_wait(&v_full[(i - 1) & 1], ((i - 1) >> 1) & 1, DEV_ERR_TIMEOUT_FULL);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          int& used = g == 0 ? used0 : used1;
+          const bool was = g == 0 ? was0 : was1, now = g == 0 ? now0 : now1;
+          if (was && ok) ok = kp_wait(&p_full[g], used & 1, DEV_ERR_TIMEOUT_ACC);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            if (was) {
+#pragma unroll
+              for (int k = 0; k < KP_KT / 16; ++k)
+                mma_f16_ts(tmem + O_COL + 128u * g, tmem + S_COL + 128u * g + 8 * k, vb + (2048 >> 4) * k, ID_O,
+                           k > 0 ? 1u : (uint32_t)used);
+            }
+            if (now) {
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k)
+                mma_f16_ss(tmem + S_COL + 128u * g,
+                           qd + g * (M::TILE >> 4) + (((k >> 2) * 16384 + (k & 3) * 32) >> 4),
+                           kb + (((k >> 2) * 16384 + (k & 3) * 32) >> 4), ID_S, k > 0);
+              mma_commit(&s_full[g]);
+            }
+            if (g == 1 && i > 0) mma_commit(&v_empty[(i - 1) & 1]);
+            if (g == 1 && more) mma_commit(&k_empty[i & 1]);
           }
           __syncwarp();
+          if (was) ++used;
         }
+        was0 = now0;
+        was1 = now1;
       }
-    } else {
-      if (warp == 8 && tiles.count > 0) {
-        // ---------------------------------------------- products
-        constexpr uint32_t ID_S = idesc_f16(128, KP_KT, false, false), ID_O = idesc_f16(128, D, false, true);
-        bool ok = kp_wait(&q_full, 0, DEV_ERR_TIMEOUT_A);
-        const uint32_t qd = desc_lo(smem_u32(sm + M::Q));
-        const uint32_t kd = desc_lo(smem_u32(sm + M::K)), vd = desc_lo(smem_u32(sm + M::V));
-        int used0 = 0, used1 = 0;                    // tiles whose weights were used, by stream
-        bool was0 = false, was1 = false;             // the last tile was one of the stream's
-        for (int i = 0; i <= tiles.count && ok; ++i) {
-          const bool more = i < tiles.count;
-          const int j0 = more ? tiles.at(i) * KP_KT : 0;
-          const bool now0 = more && rows0.any(j0, KP_KT, a.window, a.sinks);
-          const bool now1 = more && rows1.any(j0, KP_KT, a.window, a.sinks);
-          const uint32_t kb = kd + (i & 1) * (M::TILE >> 4), vb = vd + ((i - 1) & 1) * (M::TILE >> 4);
-          // every wait costs some 200 cycles here, also for what is long there: the copies' ones first,
-          // while the weights are still being computed
-          if (more) ok = kp_wait(&k_full[i & 1], (i >> 1) & 1, DEV_ERR_TIMEOUT_FULL);
-          if (i > 0 && ok) ok = kp_wait(&v_full[(i - 1) & 1], ((i - 1) >> 1) & 1, DEV_ERR_TIMEOUT_FULL);
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            int& used = g == 0 ? used0 : used1;
-            const bool was = g == 0 ? was0 : was1, now = g == 0 ? now0 : now1;
-            if (was && ok) ok = kp_wait(&p_full[g], used & 1, DEV_ERR_TIMEOUT_ACC);
-            if (!ok) break;
-            tc_fence_after();
-            if (elect_one()) {
-              if (was) {
-#pragma unroll
-                for (int k = 0; k < KP_KT / 16; ++k)
-                  mma_f16_ts(tmem + O_COL + 128u * g, tmem + S_COL + 128u * g + 8 * k, vb + (2048 >> 4) * k, ID_O,
-                             k > 0 ? 1u : (uint32_t)used);
-              }
-              if (now) {
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                  mma_f16_ss(tmem + S_COL + 128u * g,
-                             qd + g * (M::TILE >> 4) + (((k >> 2) * 16384 + (k & 3) * 32) >> 4),
-                             kb + (((k >> 2) * 16384 + (k & 3) * 32) >> 4), ID_S, k > 0);
-                mma_commit(&s_full[g]);
-              }
-              if (g == 1 && i > 0) mma_commit(&v_empty[(i - 1) & 1]);
-              if (g == 1 && more) mma_commit(&k_empty[i & 1]);
-            }
-            __syncwarp();
-            if (was) ++used;
-          }
-          was0 = now0;
-          was1 = now1;
-        }
-        // completion of everything issued, also after a wait that gave up
-        if (elect_one()) mma_commit(&all_done);
-        __syncwarp();
-        mbar_wait(&all_done, 0, DEV_ERR_TIMEOUT_ACC, false);
-      }
+      // completion of everything issued, also after a wait that gave up
+      if (elect_one()) mma_commit(&all_done);
+      __syncwarp();
+      mbar_wait(&all_done, 0, DEV_ERR_TIMEOUT_ACC, false);
     }
   }
   __syncthreads();
@@ -675,6 +683,7 @@ kv4_prefill_f32_kernel(const KvStep s, const AttnArgs a, int head0, int heads_he
   __shared__ float tile_m[4][128], fin_m[2][128], fin_l[2][128];
   uint8_t* sm = smem_align(kp_raw, 1024);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  if (kp_padding(s, a, head0, heads_here, row_tiles, 128)) return;
   if (tid == 0) {
     mbar_init(&q_full, 256);
     for (int i = 0; i < 2; ++i) {
@@ -724,11 +733,10 @@ kv4_prefill_f32_kernel(const KvStep s, const AttnArgs a, int head0, int heads_he
   const bool real = R < n_rows;
   const int64_t off = (((int64_t)b * s.L + tok) * a.heads + h * group + R - tok * group) * D;
   const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-  const bool work = r0 < n_rows;
   bool ok = true;
   float sum_m = -INFINITY;                           // the running output's maximum (warps 8-11)
 
-  if (work && warp < 8) {
+  if (warp < 8) {
     // ------------------------------------------------ scores to weights, one row a thread
     const int g = warp >> 2;
     const int64_t pr = p0 + tok;
@@ -839,7 +847,7 @@ kv4_prefill_f32_kernel(const KvStep s, const AttnArgs a, int head0, int heads_he
     }
     fin_m[g][row] = m;
     fin_l[g][row] = l;
-  } else if (work && warp < 12) {
+  } else if (warp < 12) {
     // ------------------------------------------------ the tiles' outputs into the running one
     for (int i = 0; i < tiles.count && ok; ++i) {
       ok = kp_wait(&part_full, i & 1, DEV_ERR_TIMEOUT_ACC);
@@ -863,7 +871,7 @@ kv4_prefill_f32_kernel(const KvStep s, const AttnArgs a, int head0, int heads_he
       tc_fence_before();
       mbar_arrive(&part_free);
     }
-  } else if (work && warp == 12 && tiles.count > 0) {
+  } else if (warp == 12 && tiles.count > 0) {
     // ------------------------------------------------ products
     constexpr uint32_t ID_S = idesc_f16(128, KP_KT, false, false), ID_O = idesc_f16(128, D, false, true);
     ok = kp_wait(&q_full, 0, DEV_ERR_TIMEOUT_A);
@@ -914,7 +922,7 @@ kv4_prefill_f32_kernel(const KvStep s, const AttnArgs a, int head0, int heads_he
     if (elect_one()) mma_commit(&all_done);
     __syncwarp();
     mbar_wait(&all_done, 0, DEV_ERR_TIMEOUT_ACC, false);
-  } else if (work && warp == 13) {
+  } else if (warp == 13) {
     // ------------------------------------------------ copies
     int i = 0;
     for (; i < tiles.count && ok; ++i) {
@@ -940,7 +948,7 @@ kv4_prefill_f32_kernel(const KvStep s, const AttnArgs a, int head0, int heads_he
   }
   if (!ok) failed = 1;
   __syncthreads();
-  if (work && warp >= 8 && warp < 12 && !failed) {
+  if (warp >= 8 && warp < 12 && !failed) {
     tc_fence_after();
     // the two groups' sums in the running output's scale
     float sum = 0.f;
@@ -1042,7 +1050,7 @@ static cudaError_t launch_prefill(const KvStep& s, const AttnArgs& a, uint8_t* w
 // (80 KB a tile and head); the few-query kernel takes 16 rows a warp-tile of 32 keys, which
 // cost 2.3 or 3.5 ns of the whole GPU, and 22 ns a block.  Measured, this path and the other: bf16, 128 rows of 8
 // heads, 2032 keys 46 and 21; fp32, 128 rows of 16 heads, 2128 keys 58 and 39; 512 causal fp32
-// rows of 16 heads 28 and 34; bf16, 8192 causal tokens of 8 x 4 heads 525 and 3800.
+// rows of 16 heads 24 and 34; bf16, 8192 causal tokens of 8 x 4 heads 500 and 3800.
 bool kv4_prefill_applies(const KvStep& s, const AttnArgs& a, int bf16) {
   const double rows = (double)s.L * (a.heads / a.kv_heads), heads = (double)a.kv_heads * s.B;
   double most = s.limit, mean = s.limit - 0.5 * s.L;                   // keys of a row
