@@ -27,9 +27,12 @@ namespace bitnet {
 // queries as the 8 columns, so that up to 8 queries (the heads that share a key
 // head, times a few tokens) cost one product.  A warp takes every (warps)-th tile
 // of 32 keys through its own ring of asynchronous copies; scores, weights and the
-// output stay in its registers.  The warps' partial softmaxes are merged in shared
-// memory; where several blocks share a row tile's keys, over distributed shared memory of
-// a cluster, or (many blocks a row tile) through the workspace by a second kernel.
+// output stay in its registers.  Taking the codes apart costs more than reading them
+// (16 bf16 sequences of 2048 to 32768 keys, 32 over 8 heads: 114 us, of which the memory
+// needs 46); a single short sequence is latency (513 keys, 16 heads: 7 us in a graph).
+// The warps' partial softmaxes are merged in shared memory; where several blocks share a
+// row tile's keys, over distributed shared memory of a cluster, or (many blocks a row
+// tile) through the workspace by a second kernel.
 // ---------------------------------------------------------------------------
 constexpr int KD_WARPS = 4;
 constexpr int KD_STAGES = 3;
@@ -475,7 +478,7 @@ kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e, int split
 
 // The second kernel merges the parts, a block a row: the parts' weights first, then the
 // outputs, two dimensions a thread, the parts shared between 512 / D groups of threads
-// and the groups' sums added in their order.
+// and the groups' sums added in their order.  Bound by latency: the parts lie in L2.
 constexpr int KD_MAX_SPLITS = 3 * 148;
 template <int D, int ROWS, typename XT>
 __global__ void __launch_bounds__(256)

@@ -106,7 +106,8 @@ BN_DEV KpSeen kp_seen(const KvStep& s, int b) {
 
 // ---------------------------------------------------------------------------
 // Expansion: a block a tile and key head; four warps its keys, four its values.  Bound
-// by memory (reads D + 8 bytes a key and head, writes 4 D).
+// by memory (reads D + 8 bytes a key and head, writes 4 D): 8192 keys of 8 heads in 15 us,
+// 3 % of the attention they are for.
 // ---------------------------------------------------------------------------
 // EXACT (fp32 rows): the images hold the codes themselves, and for every key the factors
 // of KpKey are written instead of the tile's.
@@ -227,7 +228,8 @@ BN_DEV bool kp_padding(const KvStep& s, const AttnArgs& a, int head0, int heads_
 // and only where their sum passes what one weight may be in fp16 (or a row sees its first
 // key) is the tile's maximum found, the output in tensor memory rescaled and the weights
 // computed once more.  (Finding every tile's maximum: 522 us for 8192 causal tokens of
-// 8 x 4 heads, so 499.)
+// 8 x 4 heads, so 499: 1.1 PFLOP/s, 67 % of a library product's rate, the rest the
+// softmax's instructions and the filling and draining of 7 blocks an SM.)
 // ---------------------------------------------------------------------------
 constexpr int KP_THREADS = 320;                      // streams: warps 0-3 and 4-7; products: warp 8; copies: warp 9
 
@@ -656,7 +658,9 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, int head0, int heads_here, 
 // four warps, each with its own scores buffer, maximum and sum; a tile's output is
 // written to a third buffer of tensor memory and added to the running one, a fourth, by
 // four more warps, with the maxima's factors.  Per tile 4 x 8 products of 128 x 128 x 16
-// (2048 cycles), which bound it.
+// (2048 cycles), which bound long contexts (8192 causal tokens of 32 over 8 heads: 1.09 ms,
+// 1000 TFLOP/s of fp16 products); 512 tokens of 16 heads are 64 blocks that spend most of
+// their 21 us filling and draining.
 // ---------------------------------------------------------------------------
 constexpr int KX_THREADS = 448;                      // weights: warps 0-3, 4-7; sums: 8-11; products: 12; copies: 13
 constexpr int KX_RING = 4;                           // tiles whose keys' factors are held
