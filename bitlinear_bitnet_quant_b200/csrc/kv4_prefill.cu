@@ -254,6 +254,15 @@ BN_DEV bool kp_wait(uint64_t* bar, uint32_t parity, int code) {
   return __all_sync(0xffffffffu, ok);
 }
 
+// Every copy that a block issued lands before the block may exit, also after waits that gave up:
+// the last N of `issued` copies, which a ring of N barriers counts.  Where the products took the
+// tiles the waits return at once.
+template <int N>
+BN_DEV void kp_copies_done(uint64_t* full, int issued) {
+  for (int i = issued > N ? issued - N : 0; i < issued; ++i)
+    mbar_wait(&full[i % N], (i / N) & 1, DEV_ERR_TIMEOUT_FULL, false);
+}
+
 // Positions of one stream's rows, and what of n keys from j0 on they see.
 struct KpRows {
   int n, p_lo, p_hi;                                 // rows; first and last position inside the cache
@@ -570,6 +579,7 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, int head0, int heads_here, 
   } else if (warp == 9) {
     // ------------------------------------------------ copies
     bool ok = true;
+    int issued[2] = {0, 0};                        // tiles of keys, of values
     for (int i = 0; i < tiles.count && ok; ++i) {
       const uint8_t* src = images + slot(i) * (2 * M::TILE);
 #pragma unroll
@@ -581,8 +591,11 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, int head0, int heads_here, 
           bulk_load(sm + (v ? M::V : M::K) + (i & 1) * M::TILE, src + v * M::TILE, M::TILE, full);
         }
         __syncwarp();
+        issued[v] += ok;
       }
     }
+    kp_copies_done<2>(k_full, issued[0]);
+    kp_copies_done<2>(v_full, issued[1]);
   } else {
     if (warp == 8 && tiles.count > 0) {
       // ---------------------------------------------- products
@@ -928,8 +941,8 @@ kv4_prefill_f32_kernel(const KvStep s, const AttnArgs a, int head0, int heads_he
     mbar_wait(&all_done, 0, DEV_ERR_TIMEOUT_ACC, false);
   } else if (warp == 13) {
     // ------------------------------------------------ copies
-    int i = 0;
-    for (; i < tiles.count && ok; ++i) {
+    int issued_k = 0, issued_v = 0;                  // tiles
+    for (int i = 0; i < tiles.count && ok; ++i) {
       const uint8_t* src = images + slot(i) * (2 * M::TILE);
       const int st = i & 1, ring = i % KX_RING;
       if (i >= 2) ok = kp_wait(&k_empty[st], ((i >> 1) - 1) & 1, DEV_ERR_TIMEOUT_EMPTY);
@@ -942,13 +955,18 @@ kv4_prefill_f32_kernel(const KvStep s, const AttnArgs a, int head0, int heads_he
         bulk_load(sm + M::K + st * M::TILE, src, M::TILE, &k_full[st]);
       }
       __syncwarp();
+      issued_k += ok;
       if (i >= 2 && ok) ok = kp_wait(&v_empty[st], ((i >> 1) - 1) & 1, DEV_ERR_TIMEOUT_EMPTY);
       if (ok && elect_one()) {
         mbar_arrive_expect_tx(&v_full[st], M::TILE);
         bulk_load(sm + M::V + st * M::TILE, src + M::TILE, M::TILE, &v_full[st]);
       }
       __syncwarp();
+      issued_v += ok;
     }
+    kp_copies_done<2>(k_full, issued_k);
+    kp_copies_done<KX_RING>(key_full, issued_k);
+    kp_copies_done<2>(v_full, issued_v);
   }
   if (!ok) failed = 1;
   __syncthreads();
