@@ -278,12 +278,16 @@ struct KpRows {
 // 2^x of a pair on the multiply-add units: x = n + r with r in [-1/2, 1/2] by adding
 // 1.5 * 2^23, a cubic for 2^r (relative error 1e-4, a fifth of the fp16 rounding that
 // follows), and n into the exponent.  x below -125 counts as -125 (2^-125 rounds to
-// zero in fp16); NaN comes out as a large number.
+// zero in fp16), x above 127 as 127: a score far above the maximum so far must show in
+// the weights' sum, and 2^n with n > 127 would run into the sign.  NaN comes out as a
+// large number.  (The upper bound costs 0.7 % of 8192 causal tokens.)
 BN_DEV void exp2_pair(uint64_t x, float& e0, float& e1) {
   float a, b;
   unpack_f2(x, a, b);
   asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(-125.f));
   asm("max.NaN.f32 %0, %0, %1;" : "+f"(b) : "f"(-125.f));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(127.f));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(b) : "f"(127.f));
   const uint64_t v = pack_f2(a, b);
   const uint64_t big = pack_f2(12582912.f, 12582912.f), nbig = pack_f2(-12582912.f, -12582912.f);
   const uint64_t t = add_f2(v, big);

@@ -1,0 +1,124 @@
+"""The key/value step on the GPU where it is easily wrong: scores that jump from one
+tile of keys to the next, steps, queries and rows that are not finite, positions
+outside the cache, bounds on positions, callers' workspaces, heads in several turns,
+and the layers over ragged and captured steps.  Against float64.
+
+Bounds (u = 2^-24; half steps: fp16 2^-11, bf16 2^-8).  A score: fp32 queries in two
+fp16 terms 2^-22, 2d products summed with truncation 2d * 2^-23, four factors u, each
+of m = max_j sum_i |q_i k_ij| / sqrt(d); its base-2 form y rounds three times, 3 |y| u
+ln 2 of e^score.  A weight is off by twice that (its own score and the largest one) and
+2^-21 for the exponential and its fp16 terms; bf16 rows take one term, 2^-11, and with
+many queries values and keys of 11 bits (2^-11 each: the keys' of m, unless they are
+exact) and a cubic for some exponentials, 7.6e-5.  Sums over n keys: 3 n 2^-23.  The
+output is within twice the weights' bound of sum_j w_j |v_j|, and 2^-8 (bf16) or 2u of
+itself.
+"""
+import math
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from bitlinear_bitnet_quant_b200 import api, build_lib  # noqa: E402
+from bitlinear_bitnet_quant_b200 import workloads as wl  # noqa: E402
+from oracle import kv4_oracle as KO  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+F32, BF16 = torch.float32, torch.bfloat16
+KERNELS = pytest.mark.parametrize("kernel", [1, 2])
+DTYPES = pytest.mark.parametrize("dtype", [F32, BF16])
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build_lib.build()
+    api.lib()
+    yield
+    assert api.bitnet_device_error() == 0
+
+
+def host(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def normal(rng, n, width, dtype, scale=1.0):
+    return torch.from_numpy((rng.standard_normal((n, width)) * scale).astype(np.float32)).cuda().to(dtype)
+
+
+def codes(rng, *shape):
+    return np.clip(np.rint(rng.standard_normal(shape) * 2.6), -8, 7).astype(np.int8)
+
+
+def hold(kc, ks, vc, vs):
+    """The cache of codes [B, kv, T, d] and steps [B, kv, T], and the values it stands for."""
+    dev = api.KV4Cache(*(torch.from_numpy(np.ascontiguousarray(x)).cuda() for x in
+                         (KO.pack_codes(kc), ks.astype(np.float32), KO.pack_codes(vc), vs.astype(np.float32))))
+    return dev, kc * ks.astype(np.float32).astype(np.float64)[..., None], \
+        vc * vs.astype(np.float32).astype(np.float64)[..., None]
+
+
+def steps(rng, *shape):
+    return rng.uniform(0.1, 0.9, shape)
+
+
+def check(got, q, k, v, positions, kernel, dtype, window=0, sinks=0, exact_keys=False):
+    """got, q [n, heads, d] of one sequence; k, v [kv, T, d]."""
+    kv, T, d = k.shape
+    heads, bf16, many = q.shape[1], dtype == BF16, kernel != 1 and dtype == BF16
+    see = KO.visible(np.where((positions >= 0) & (positions < T), positions, -1), T, window, sinks)
+    for h in range(heads):
+        ref, wv, m = KO.attention(q[:, h], k[h // (heads // kv)], v[h // (heads // kv)], see)
+        E = (2.0 ** -22 + 2 * d * 2.0 ** -23 + 4 * U + (many and not exact_keys) * 2.0 ** -11) * m
+        E = E + 3 * (m / math.log(2) + 256) * U * math.log(2)
+        w = 2 * E + 2.0 ** -21 + 3 * see.sum(-1) * 2.0 ** -23 + bf16 * 2.0 ** -11 + many * (2.0 ** -11 + 7.6e-5)
+        tol = 2 * w[:, None] * wv + (2.0 ** -8 if bf16 else 2 * U) * np.abs(ref) + 1e-30
+        err = np.abs(got[:, h] - ref)
+        assert np.all(err <= tol), (h, (err / tol).max())
+
+
+# ------------------------------------------------------- scores that jump --
+
+# The spike's score in base 2 is 16.3 c 2^e and its value step 2^F, the others' scores are near zero: the
+# last three pass 2^127 of the maximum so far
+@KERNELS
+@DTYPES
+@pytest.mark.parametrize("c,e,F", [(1, 0, -1), (7, 0, -1), (1, 3, -1), (3, 2, -1), (5, 2, -1), (1, 5, -1), (3, 0, 59),
+                                   (1, 2, 59), (7, 5, 59)])
+def test_a_score_far_above_the_tiles_before(c, e, F, dtype, kernel):
+    """One key of a later tile that carries all the weight, at every place of eight."""
+    rng = np.random.default_rng(100 * c + e)
+    B, L, T, d = 16, 33, 432, 128
+    base = -15 if F > 0 else -1                      # the other value steps
+    kc, vc = codes(rng, B, 1, T, d), codes(rng, B, 1, T, d)
+    ks, vs = np.full((B, 1, T), 2.0 ** -6), 2.0 ** base * rng.uniform(1, 2, (B, 1, T))
+    for b in range(B):
+        j = (128 if b < 8 else 312) + b % 8
+        kc[b, 0, j], ks[b, 0, j], vs[b, 0, j] = c, 2.0 ** e, 2.0 ** F * 1.5
+    vc[vc == 0] = 1                                  # (no output that only the keys of tiny weights make)
+    cache, k, v = hold(kc, ks, vc, vs)
+    q = torch.ones((B * L, d), dtype=dtype, device="cuda")
+    A = host(api.bitnet_kv4_attention(q, cache, B, L, T - L, 1, kernel=kernel)).reshape(B, L, 1, d)
+    for b in range(B):
+        check(A[b], host(q).reshape(B, L, 1, d)[b], k[b], v[b], T - L + np.arange(L), kernel, dtype, exact_keys=True)
+
+
+@KERNELS
+@DTYPES
+@pytest.mark.parametrize("size,window", [(2.0 ** -8, 0), (2.0 ** -4, 0), (2.0 ** -2, 0), (2.0 ** -4, 200)])
+def test_scores_that_grow_along_the_keys(size, window, dtype, kernel):
+    """Key j's score in base 2 is 16.3 j size: every key carries most of the weight of its own query."""
+    rng = np.random.default_rng(7)
+    L, T, d = 300, 432, 128
+    kc, vc = np.ones((1, 1, T, d), dtype=np.int8), codes(rng, 1, 1, T, d)
+    vc[vc == 0] = 1
+    cache, k, v = hold(kc, np.arange(T)[None, None] * size, vc, steps(rng, 1, 1, T))
+    q = torch.ones((L, d), dtype=dtype, device="cuda")
+    A = host(api.bitnet_kv4_attention(q, cache, 1, L, T - L, 1, window=window, sinks=3, kernel=kernel)).reshape(L, 1, d)
+    check(A, np.ones((L, 1, d)), k[0], v[0], T - L + np.arange(L), kernel, dtype, window, 3, exact_keys=True)
