@@ -275,13 +275,15 @@ kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e, int split
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int key = 16 * x + 8 * y + g;
-        const float kstep = kst[key], vstep = vst[key];
+        // a step that is not finite is NaN to the queries that see the key, through the score (inf 0 = NaN),
+        // and finite in the operand, where a hidden key's weight is zero
+        const float vstep = vst[key], both = fmaf(vstep, 0.f, kst[key]), kstep = fmaf(both, 0.f, both);
         // the exponent field, clamped as in step_exponent; as a float through the low bits of 2^23
         int e = (int)(__float_as_uint(vstep) >> 23);
         e = e < 103 ? 103 : (e > 253 ? 253 : e);
         const float ef = __uint_as_float(0x4B000000u + (uint32_t)e) - 8388735.f;
         inv[x][y] = __uint_as_float((uint32_t)(254 - e) << 23);
-        f[x][y] = vstep * inv[x][y];
+        f[x][y] = fminf(fabsf(vstep) * inv[x][y], 2.f);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -291,17 +293,13 @@ kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e, int split
             sc[x][n][2 * y + i] = acc * (kstep * unscale[n][i]) + ef;
           }
         if (!full) {
-          // masked scores; a value step that is not finite is NaN to the queries that see the key, through
-          // the score, and zero in the operand
-          const bool finite = fabsf(vstep) < INFINITY;
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               float& v = sc[x][n][2 * y + i];
-              v = !key_visible(j0 + key, pos[n][i], a.window, a.sinks) ? -INFINITY : finite ? v : NAN;
+              v = key_visible(j0 + key, pos[n][i], a.window, a.sinks) ? v : -INFINITY;
             }
-          if (!finite) f[x][y] = 0.f;
         }
       }
     // ---- running maximum (a query's keys lie in the 8 lanes of one t), weights, sums ----

@@ -122,3 +122,36 @@ def test_scores_that_grow_along_the_keys(size, window, dtype, kernel):
     q = torch.ones((L, d), dtype=dtype, device="cuda")
     A = host(api.bitnet_kv4_attention(q, cache, 1, L, T - L, 1, window=window, sinks=3, kernel=kernel)).reshape(L, 1, d)
     check(A, np.ones((L, 1, d)), k[0], v[0], T - L + np.arange(L), kernel, dtype, window, 3, exact_keys=True)
+
+
+# ------------------------------------------- what is not finite, by its place --
+
+@KERNELS
+@DTYPES
+@pytest.mark.parametrize("bad", [math.inf, math.nan])
+@pytest.mark.parametrize("L,t0,j", [(1, 400, 5), (1, 400, 399), (40, 300, 7), (40, 300, 310), (150, 0, 3), (150, 0, 70),
+                                    (150, 0, 140)])
+def test_a_step_that_is_not_finite(L, t0, j, bad, dtype, kernel):
+    """Makes exactly the queries that see its key NaN, in tiles that they see whole and in others."""
+    rng = np.random.default_rng(31)
+    heads, kv, d, T = 8, 2, 128, 448
+    clean = [codes(rng, 1, kv, T, d), steps(rng, 1, kv, T), codes(rng, 1, kv, T, d), steps(rng, 1, kv, T)]
+    q = normal(rng, L, heads * d, dtype, 1.5)
+    at = t0 + np.arange(L)
+    for which in (1, 3):
+        parts = [x.copy() for x in clean]
+        parts[which][0, :, j] = bad
+        cache, k, v = hold(*parts)
+        A = host(api.bitnet_kv4_attention(q, cache, 1, L, t0, heads, kernel=kernel)).reshape(L, heads, d)
+        assert np.isnan(A[at >= j]).all()
+        before = at < j
+        if before.any():
+            check(A[before], host(q).reshape(L, heads, d)[before], k[0, :, :j], v[0, :, :j], at[before], kernel, dtype)
+    # behind the last query the same steps, and negative ones, are not seen
+    parts = [x.copy() for x in clean]
+    for which in (1, 3):
+        parts[which][0, :, t0 + L:] = bad
+        parts[which][0, :, t0 + L] = -math.inf
+    cache, k, v = hold(*parts)
+    A = host(api.bitnet_kv4_attention(q, cache, 1, L, t0, heads, kernel=kernel)).reshape(L, heads, d)
+    check(A, host(q).reshape(L, heads, d), k[0, :, :t0 + L], v[0, :, :t0 + L], at, kernel, dtype)
