@@ -540,7 +540,9 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, int head0, int heads_here, 
     // ---- the output, divided by the sum ----
     if (ok && used > 0) ok = kp_wait(&all_done, 0, DEV_ERR_TIMEOUT_ACC);
     tc_fence_after();
-    float inv = m == -INFINITY && l == 0.f ? 0.f : 0x1p-11f / l;      // a query that sees no key: zeros
+    // a query outside the cache sees no key: zeros, whatever the masked keys' exponentials (2^-125 where they
+    // come from the multiply-add units) left in its sum
+    float inv = p < 0 ? 0.f : 0x1p-11f / l;
     // (through the queries' shared memory, free by now, to runs of lanes)
     uint8_t* stage = sm + M::Q + g * M::TILE;
 #pragma unroll 1

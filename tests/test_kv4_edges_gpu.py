@@ -155,3 +155,22 @@ def test_a_step_that_is_not_finite(L, t0, j, bad, dtype, kernel):
     cache, k, v = hold(*parts)
     A = host(api.bitnet_kv4_attention(q, cache, 1, L, t0, heads, kernel=kernel)).reshape(L, heads, d)
     check(A, host(q).reshape(L, heads, d), k[0, :, :t0 + L], v[0, :, :t0 + L], at, kernel, dtype)
+
+
+@KERNELS
+@DTYPES
+@pytest.mark.parametrize("e", [0, 19, 20, 24, 28, 30, 58])
+def test_rows_outside_the_cache_are_zero_beside_large_values(e, dtype, kernel):
+    """Value steps of 2^e; some of a block's positions before or behind the cache, or at and past the bound."""
+    rng = np.random.default_rng(41)
+    L, heads, d, T = 150, 2, 64, 160
+    cache, k, v = hold(codes(rng, 1, 1, T, d), steps(rng, 1, 1, T), codes(rng, 1, 1, T, d),
+                       2.0 ** e * rng.uniform(1, 2, (1, 1, T)))
+    q = normal(rng, L, heads * d, dtype, 1.5)
+    for first, t_max in ((T - 60, None), (-40, None), (0, 100), (20, 129)):
+        A = host(api.bitnet_kv4_attention(q, cache, 1, L, 0, heads, t_max=t_max, pos=ints([first]),
+                                          kernel=kernel)).reshape(L, heads, d)
+        at = first + np.arange(L)
+        inside = (at >= 0) & (at < (t_max or T))
+        assert not A[~inside].any() and not np.isnan(A).any()
+        check(A[inside], host(q).reshape(L, heads, d)[inside], k[0], v[0], at[inside], kernel, dtype)
