@@ -462,8 +462,9 @@ kv4_decode_kernel(const KvStep s, const AttnArgs a, float scale_log2e, int split
       x0 += w * ld_cluster_f32(oa);
       x1 += w * ld_cluster_f32(oa + 4);
     }
-    const float r = mx == -INFINITY && sum == 0.f ? 0.f : 1.0f / sum;    // a query that sees no key: zeros
     const int R = r0 + row, tok = R / group;
+    // a query outside the cache sees no key: zeros; scores that are all -inf leave 0 / 0
+    const float r = p0 + tok < 0 || p0 + tok >= s.limit ? 0.f : 1.0f / sum;
     const int64_t off = (((int64_t)b * s.L + tok) * a.heads + h * group + R - tok * group) * D + dim;
     if constexpr (SPLIT) {
       *reinterpret_cast<float2*>(static_cast<float*>(a.A) + off) = make_float2(x0 * r, x1 * r);
@@ -522,8 +523,10 @@ kv4_merge_kernel(const KvStep s, const AttnArgs a, int splits, const float* part
     x.x += x_part[i][pair].x;
     x.y += x_part[i][pair].y;
   }
-  const float r = mx == -INFINITY && sum == 0.f ? 0.f : 1.0f / sum;        // a query that sees no key: zeros
   const int tok = R / group;
+  // a query outside the cache sees no key: zeros; scores that are all -inf leave 0 / 0
+  const int64_t at = kv_first_position(s, b) + tok;
+  const float r = at < 0 || at >= s.limit ? 0.f : 1.0f / sum;
   const int64_t off = (((int64_t)b * s.L + tok) * a.heads + h * group + R - tok * group) * D + 2 * pair;
   if constexpr (sizeof(XT) == 4) {
     *reinterpret_cast<float2*>(static_cast<float*>(a.A) + off) = make_float2(x.x * r, x.y * r);

@@ -542,7 +542,8 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, int head0, int heads_here, 
     tc_fence_after();
     // a query outside the cache sees no key: zeros, whatever the masked keys' exponentials (2^-125 where they
     // come from the multiply-add units) left in its sum
-    float inv = p < 0 ? 0.f : 0x1p-11f / l;
+    // (a maximum of -inf: scores that are all past the smallest fp32 number, or NaN)
+    float inv = p < 0 ? 0.f : m == -INFINITY ? NAN : 0x1p-11f / l;
     // (through the queries' shared memory, free by now, to runs of lanes)
     uint8_t* stage = sm + M::Q + g * M::TILE;
 #pragma unroll 1
@@ -983,7 +984,9 @@ kv4_prefill_f32_kernel(const KvStep s, const AttnArgs a, int head0, int heads_he
 #pragma unroll
     for (int g = 0; g < 2; ++g)
       if (fin_m[g][row] != -INFINITY || fin_l[g][row] != 0.f) sum += fin_l[g][row] * ex2(fin_m[g][row] - sum_m);
-    float inv = sum_m == -INFINITY && sum == 0.f ? 0.f : 1.0f / sum;   // a query that sees no key: zeros
+    // a query outside the cache sees no key: zeros; scores that are all -inf leave 0 / 0
+    const int64_t pr = p0 + tok;
+    float inv = pr < 0 || pr >= s.limit ? 0.f : 1.0f / sum;
     // (through the queries' shared memory, free by now, to runs of lanes)
     uint8_t* stage = sm + M::Q;
 #pragma unroll 1

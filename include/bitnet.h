@@ -406,8 +406,10 @@ BITNET_API int bitnet_kv4_read(const uint8_t* Kc, const float* Ks, const uint8_t
  *   (a sliding window behind a few first tokens that stay visible).  The cache must
  *   hold the keys up to the step's own already, with steps as bitnet_kv4_append
  *   writes them (0, or 1e-5 / 7 and more; below 2^60).  A row is NaN where its query,
- *   or the step of a key that it sees, is not finite or its scores pass the range of
- *   fp32; no other row is touched by that.
+ *   or the step of a key that it sees, is not finite, and where one of its scores is past
+ *   the largest fp32 number or all of them past the smallest; single ones past the
+ *   smallest weigh nothing.  (Where a row's largest |q| times a step that it sees passes
+ *   2^126, a product of zero may count as NaN.)  No other row is touched by that.
  * Q, A   : [B*L][heads*d] in dtype (A may be Q itself).
  * window : 0 (every key) or the number of keys of the window; sinks >= 0.
  * t_max  : a bound on the positions in use plus one, 1 .. T_cap, or 0 (T_cap): a

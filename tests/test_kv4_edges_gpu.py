@@ -174,3 +174,46 @@ def test_rows_outside_the_cache_are_zero_beside_large_values(e, dtype, kernel):
         inside = (at >= 0) & (at < (t_max or T))
         assert not A[~inside].any() and not np.isnan(A).any()
         check(A[inside], host(q).reshape(L, heads, d)[inside], k[0], v[0], at[inside], kernel, dtype)
+
+
+@KERNELS
+@DTYPES
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_past_the_range_of_fp32(sign, dtype, kernel):
+    """Every score of a row past the range, to either side: NaN.  One past the smallest number
+    beside finite ones weighs nothing."""
+    rng = np.random.default_rng(51)
+    T, d = 144, 128
+    for L, t0 in ((1, 130), (140, 0)):
+        kc, ks = np.full((1, 1, T, d), sign, dtype=np.int8), np.full((1, 1, T), 2.0 ** 59)
+        vc, vs = codes(rng, 1, 1, T, d), steps(rng, 1, 1, T)
+        q = torch.full((L, d), 1e38, dtype=dtype, device="cuda")
+        A = api.bitnet_kv4_attention(q, hold(kc, ks, vc, vs)[0], 1, L, t0, 1, kernel=kernel)
+        assert A.isnan().all()
+        if sign < 0:                                 # a key whose score is zero
+            kc[0, 0, 2] = 0
+            cache, k, v = hold(kc, ks * np.where(np.arange(T) == 2, 2.0 ** -59, 1.0), vc, vs)
+            A = host(api.bitnet_kv4_attention(q, cache, 1, L, t0, 1, kernel=kernel))
+            at = t0 + np.arange(L)
+            assert np.isnan(A[at < 2]).all()
+            assert np.all(np.abs(A[at >= 2] - v[0, 0, 2]) <= (2.0 ** -8 + 2.0 ** -10) * np.abs(v[0, 0, 2]))
+
+
+@KERNELS
+@DTYPES
+def test_an_infinite_query_is_nan(dtype, kernel):
+    """Also where every score is -inf."""
+    rng = np.random.default_rng(52)
+    T, d, heads = 144, 64, 2
+    for L, t0 in ((1, 0), (1, 130), (140, 0)):
+        kc = codes(rng, 1, 1, T, d)
+        kc[..., 9] = -3
+        cache, k, v = hold(kc, steps(rng, 1, 1, T), codes(rng, 1, 1, T, d), steps(rng, 1, 1, T))
+        for bad in (math.inf, -math.inf):
+            q = normal(rng, L, heads * d, dtype)
+            q[-1, d + 9] = bad                       # the last token's second head
+            A = host(api.bitnet_kv4_attention(q, cache, 1, L, t0, heads, kernel=kernel)).reshape(L, heads, d)
+            assert np.isnan(A[-1, 1]).all()
+            qh = host(q).reshape(L, heads, d)
+            check(A[:, :1], qh[:, :1], k[0], v[0], t0 + np.arange(L), kernel, dtype)
+            check(A[:-1, 1:], qh[:-1, 1:], k[0], v[0], t0 + np.arange(L - 1), kernel, dtype)
