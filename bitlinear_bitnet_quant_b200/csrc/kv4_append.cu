@@ -183,17 +183,18 @@ BN_DEV void turn_row(const float (&x)[8], float (&t)[8], int q, int norm, const 
 // rint(t s) + 8 stands in the low bits of t s + (1.5 * 2^23 + 8), rounded to nearest even;
 // the shifted sum of eight such words, less that of their constant parts (modulo 2^32),
 // is the word of biased codes.  |t s| <= 7 up to its rounding, so that no code needs the
-// clamp to -8 .. 7.
+// clamp to -8 .. 7.  A row with a value that is not finite gets the step NaN, whatever its
+// codes: it stands for NaN, as the rule's inf * 0 and NaN do.
 template <int D>
 BN_DEV uint32_t row_to_codes(const float (&t)[8], float& step) {
   constexpr int LPH = D / 8;
   float mx = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(t[i]));
+  for (int i = 0; i < 8; i += 2) mx = max3_nan(mx, fabsf(t[i]), fabsf(t[i + 1]));
 #pragma unroll
-  for (int o = 1; o < LPH; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  for (int o = 1; o < LPH; o <<= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   const float s = __fdiv_rn(7.0f, fmaxf(mx, 1e-5f));
-  step = __fdiv_rn(1.0f, s);
+  step = mx < INFINITY ? __fdiv_rn(1.0f, s) : NAN;
   uint32_t w = 0u, constant = 0u;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {

@@ -354,7 +354,8 @@ BITNET_API int bitnet_attention(const float* Q, const float* Kc, const float* Vc
  *   4 bits    t = fp32(y);  s = 7 / max(max|t|, 1e-5);  code = clamp(rint(t * s),
  *             -8, 7);  step = 1 / s.  The row stands for code * step.
  *   Keys of the 4-bit cache are computed in fp64 up to t, queries and fp32 caches
- *   in fp32 (angles in fp64).  Values are finite.
+ *   in fp32 (angles in fp64).  A row with a NaN or an infinity gets the step NaN: it
+ *   reads back as NaN and makes the queries that see it NaN.
  * 4-bit caches: codes Kc, Vc [B][kv_heads][T_cap][d/2] bytes, steps Ks, Vs
  *   [B][kv_heads][T_cap] fp32, T_cap % 16 == 0.  Of each 8 codes of a row (one
  *   little-endian 32-bit word), code 2j + i (i = 0, 1) sits at bits 4j + 16i, two's

@@ -217,3 +217,35 @@ def test_an_infinite_query_is_nan(dtype, kernel):
             qh = host(q).reshape(L, heads, d)
             check(A[:, :1], qh[:, :1], k[0], v[0], t0 + np.arange(L), kernel, dtype)
             check(A[:-1, 1:], qh[:-1, 1:], k[0], v[0], t0 + np.arange(L - 1), kernel, dtype)
+
+
+@pytest.mark.parametrize("dtype,d,norm,had,B,L", [(F32, 128, False, False, 2, 5), (BF16, 64, True, True, 1, 40),
+                                                  (BF16, 128, False, True, 2, 700), (F32, 64, True, False, 3, 1)])
+def test_append_keeps_what_is_not_finite(dtype, d, norm, had, B, L):
+    """A key or value row with a NaN or an infinity is held with the step NaN, reads back as NaN and makes the
+    queries that see it NaN; every other row is held as without it."""
+    rng = np.random.default_rng(61)
+    heads, kv, n = 4, 2, B * L
+    q, k, v = (normal(rng, n, w * d, dtype) for w in (heads, kv, kv))
+    kw = dict(norm=norm, hadamard=had)
+    T = L + 16
+    clean, cache = api.bitnet_kv4_cache(B, T, kv, d), api.bitnet_kv4_cache(B, T, kv, d)
+    api.bitnet_kv4_append(q, k, v, clean, B, L, 0, heads, **kw)
+    bad_k, bad_v = torch.zeros((n, kv), dtype=torch.bool, device="cuda"), torch.zeros((n, kv), dtype=torch.bool, device="cuda")
+    for i, (x, seen, val) in enumerate([(k, bad_k, math.nan), (k, bad_k, math.inf), (v, bad_v, math.nan),
+                                        (v, bad_v, -math.inf)]):
+        r, h = (5 * i + 2) % n, i % kv
+        x[r, h * d + 7 * i + 3] = val
+        seen[r, h] = True
+    Qo = api.bitnet_kv4_append(q, k, v, cache, B, L, 0, heads, **kw)
+    K, V = api.bitnet_kv4_read(cache, B, L, 0)
+    for bad, got, c, s, c0, s0 in ((bad_k, K, cache.kc, cache.ks, clean.kc, clean.ks),
+                                   (bad_v, V, cache.vc, cache.vs, clean.vc, clean.vs)):
+        held = bad.view(B, L, kv).transpose(1, 2)
+        assert torch.equal(s[:, :, :L].isnan(), held)
+        assert torch.equal(got.view(n, kv, d).isnan(), bad[:, :, None].expand(n, kv, d))
+        assert torch.equal(c[:, :, :L][~held], c0[:, :, :L][~held]) and torch.equal(s[:, :, :L][~held], s0[:, :, :L][~held])
+    sees = (bad_k | bad_v).view(B, L, kv).int().cummax(1).values.bool().repeat_interleave(heads // kv, -1)
+    for kernel in (1, 2):
+        A = api.bitnet_kv4_attention(Qo, cache, B, L, 0, heads, kernel=kernel).view(B, L, heads, d)
+        assert torch.equal(A.isnan(), sees[..., None].expand(B, L, heads, d))
