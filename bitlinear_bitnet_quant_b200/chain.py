@@ -84,7 +84,7 @@ class BitLinearChain:
             else:
                 raise ValueError("kv_bits is 32 or 4")
         self.t0 = 0
-        self.pos = self.lens = None
+        self.pos = self.lens = self.t_max = None
         f32 = dict(dtype=torch.float32, device=device)
         e = lambda *shape: torch.empty(shape, **f32)
         self.x = [e(M, hidden), e(M, hidden)]          # layer input, chain output
@@ -137,7 +137,7 @@ class BitLinearChain:
             A.bitnet_kv4_append(self.q, self.k, self.v, self.kv4[index], B, L, self.t0, self.heads, norm=self.qk_norm,
                                 hadamard=self.hadamard, Qo=self.q, **norm, **at)
             return A.bitnet_kv4_attention(self.q, self.kv4[index], B, L, self.t0, self.heads, self.window, self.sinks,
-                                          A=self.att, **at)
+                                          t_max=self.t_max, A=self.att, **at)
         if self.qk_norm:
             A.bitnet_qk_norm_rope_append(self.q, self.k, self.v, self.kc[index], self.vc[index], B, L, self.t0,
                                          self.heads, Qo=self.q, stream=s, **norm)
@@ -147,15 +147,17 @@ class BitLinearChain:
         return A.bitnet_attention(self.q, self.kc[index], self.vc[index], B, L, self.t0, self.heads, A=self.att,
                                   stream=s)
 
-    def forward(self, x: torch.Tensor, stream=None, t0: int = 0, pos=None, lens=None) -> torch.Tensor:
+    def forward(self, x: torch.Tensor, stream=None, t0: int = 0, pos=None, lens=None, t_max=None) -> torch.Tensor:
         """x: [M, hidden] fp32 on the device; returns the last layer's output
         (one of the chain's own buffers).  t0: position of each sequence's first
         token in this step (with attention).  With kv_bits 4, pos and lens ([B] int32
         on the device) place each sequence's tokens at t0 + pos[b] on and mark the rows
-        behind its first lens[b] as padding; a captured forward reads them at replay."""
-        if (pos is not None or lens is not None) and (self.attention is None or self.kv_bits != 4):
-            raise ValueError("pos and lens need attention with kv_bits=4")
-        self.t0, self.pos, self.lens = t0, pos, lens
+        behind its first lens[b] as padding; a captured forward reads them at replay.
+        t_max: a bound on the positions in use plus one (api.bitnet_kv4_attention), for
+        which the attention's kernels are chosen; with pos and without it that is T_cap."""
+        if not (pos is None and lens is None and t_max is None) and (self.attention is None or self.kv_bits != 4):
+            raise ValueError("pos, lens and t_max need attention with kv_bits=4")
+        self.t0, self.pos, self.lens, self.t_max = t0, pos, lens, t_max
         parts = (x,)
         for i, w in enumerate(self.layers):
             parts = self.layer(parts, w, stream, i)
