@@ -60,8 +60,8 @@ def hold(kc, ks, vc, vs):
     """The cache of codes [B, kv, T, d] and steps [B, kv, T], and the values it stands for."""
     dev = api.KV4Cache(*(torch.from_numpy(np.ascontiguousarray(x)).cuda() for x in
                          (KO.pack_codes(kc), ks.astype(np.float32), KO.pack_codes(vc), vs.astype(np.float32))))
-    return dev, kc * ks.astype(np.float32).astype(np.float64)[..., None], \
-        vc * vs.astype(np.float32).astype(np.float64)[..., None]
+    with np.errstate(invalid="ignore"):              # (a code 0 of an infinite step)
+        return dev, *(c * s.astype(np.float32).astype(np.float64)[..., None] for c, s in ((kc, ks), (vc, vs)))
 
 
 def steps(rng, *shape):
@@ -249,3 +249,134 @@ def test_append_keeps_what_is_not_finite(dtype, d, norm, had, B, L):
     for kernel in (1, 2):
         A = api.bitnet_kv4_attention(Qo, cache, B, L, 0, heads, kernel=kernel).view(B, L, heads, d)
         assert torch.equal(A.isnan(), sees[..., None].expand(B, L, heads, d))
+
+
+# --------------------------------------- bounds, workspaces, heads in turns --
+
+@KERNELS
+@DTYPES
+@pytest.mark.parametrize("B,L,ctx,T", [(1, 1, 300, 8192), (2, 70, 500, 2048)])
+def test_a_bound_on_the_positions_and_a_callers_workspace(B, L, ctx, T, dtype, kernel):
+    """Any bound past the last position gives the attention within its bounds; rows at and past a smaller one are zero.
+    A workspace of the size asked for is enough and nothing behind it is written; a byte less is refused."""
+    rng = np.random.default_rng(71)
+    heads, kv, d = 4, 2, 128
+    cache, k, v = hold(codes(rng, B, kv, T, d), steps(rng, B, kv, T), codes(rng, B, kv, T, d), steps(rng, B, kv, T))
+    q = normal(rng, B * L, heads * d, dtype, 1.5)
+    before = [ctx - 7 * b for b in range(B)]
+    for t_max in (ctx + L, ctx + L + 130, T - 1, T, 0):
+        need = api.bitnet_kv4_attention_workspace_size(dtype, B, L, heads, kv, d, T, t_max=t_max, kernel=kernel)
+        room = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+        A = api.bitnet_kv4_attention(q, cache, B, L, 0, heads, t_max=t_max, pos=ints(before), workspace=room[:need],
+                                     kernel=kernel)
+        assert bool((room[need:] == 0xA5).all())
+        for b in range(B):
+            check(host(A).reshape(B, L, heads, d)[b], host(q).reshape(B, L, heads, d)[b], k[b], v[b],
+                  before[b] + np.arange(L), kernel, dtype)
+        own = api.bitnet_kv4_attention(q, cache, B, L, 0, heads, t_max=t_max, pos=ints(before), kernel=kernel)
+        assert torch.equal(own, A)
+        if need:
+            with pytest.raises(api.BitnetError):
+                api.bitnet_kv4_attention(q, cache, B, L, 0, heads, t_max=t_max, pos=ints(before),
+                                         workspace=room[:need - 1], kernel=kernel)
+    A = host(api.bitnet_kv4_attention(q, cache, B, L, 0, heads, t_max=ctx + L - 1, pos=ints(before), kernel=kernel))
+    A = A.reshape(B, L, heads, d)
+    assert not A[0, -1].any() and A[0, :-1].any(-1).all() and A[1:].any(-1).all()
+
+
+@DTYPES
+def test_heads_in_several_turns(dtype):
+    """Ten heads of 65536 keys: more than a workspace of 256 MB holds at once."""
+    g = torch.Generator(device="cuda").manual_seed(81)
+    rng = np.random.default_rng(81)
+    kv, T, d, L = 10, 65536, 128, 20
+    one = api.bitnet_kv4_attention_workspace_size(dtype, 1, L, 1, 1, d, T, kernel=2)
+    need = api.bitnet_kv4_attention_workspace_size(dtype, 1, L, kv, kv, d, T, kernel=2)
+    assert one < need < kv * one and need % one == 0
+    half = lambda: (torch.randint(0, 256, (1, kv, T, d // 2), generator=g, device="cuda", dtype=torch.uint8),
+                    torch.rand((1, kv, T), generator=g, device="cuda") * 0.2 + 0.1)
+    cache = api.KV4Cache(*half(), *half())
+    q = normal(rng, L, kv * d, dtype, 1.5)
+    A = api.bitnet_kv4_attention(q, cache, 1, L, T - L, kv, kernel=2)
+    got, qh = host(A).reshape(L, kv, d), host(q).reshape(L, kv, d)
+    turn = need // one
+    for h in (0, turn - 1, turn, kv - 1):            # the ends of the turns
+        k, v = (KO.unpack_codes(c[0, h].cpu().numpy()) * host(s)[0, h, :, None]
+                for c, s in ((cache.kc, cache.ks), (cache.vc, cache.vs)))
+        check(got[:, h:h + 1], qh[:, h:h + 1], k[None], v[None], T - L + np.arange(L), 2, dtype)
+    # more workspace, fewer turns: the same rows
+    room = torch.empty(kv * one, dtype=torch.uint8, device="cuda")
+    assert torch.equal(api.bitnet_kv4_attention(q, cache, 1, L, T - L, kv, workspace=room, kernel=2), A)
+
+
+# ------------------------------------------------------------- the layers --
+
+def _chain(rng, B, L, T, kv_heads, n_layers=1, **att):
+    from bitlinear_bitnet_quant_b200 import chain
+    H, F, d = 2048, 512, 128
+    sizes = dict(q=(H, H), k=(kv_heads * d, H), v=(kv_heads * d, H), o=(H, H), up=(F, H), gate=(F, H), down=(H, F))
+    layers = [chain.quantize_layer({n: torch.from_numpy(wl.gaussian(rng, s, 0.02)).cuda() for n, s in sizes.items()})
+              for _ in range(n_layers)]
+    make = lambda L: chain.BitLinearChain(layers, B * L, H, F, torch.device("cuda"), attention=dict(
+        B=B, L=L, T_cap=T, heads=16, kv_bits=4, kv_heads=kv_heads, **att))
+    return [make(l) for l in L]
+
+
+def test_chain_over_a_ragged_step():
+    """A padded batch of prompts, then a step of one token behind each: what the caches hold and the attention's
+    rows against float64, with the same steps of the chain's own call."""
+    rng = np.random.default_rng(91)
+    B, L, T, kv, d = 3, 30, 64, 4, 128
+    pre, dec = _chain(rng, B, (L, 1), T, kv, window=20, sinks=2, qk_norm=True)
+    dec.kv4 = pre.kv4
+    new = [30, 11, 1]
+    for ch, Ls, pos, lens in ((pre, L, [0] * B, new), (dec, 1, new, [1, 0, 1])):
+        x = torch.from_numpy(wl.gaussian(rng, (B * Ls, 2048))).cuda()
+        held = [t.clone() for t in ch.kv4[0]]
+        out = ch.forward(x, pos=ints(pos), lens=ints(lens))
+        for b in range(B):
+            assert torch.isfinite(out[b * Ls:b * Ls + lens[b]]).all()
+            n = pos[b] + lens[b]
+            for t, was in zip(ch.kv4[0], held):      # nothing but the real tokens' rows is written
+                assert torch.equal(t[b, :, :pos[b]], was[b, :, :pos[b]]) and torch.equal(t[b, :, n:], was[b, :, n:])
+            if not lens[b]:
+                continue
+            sl = slice(b * Ls, b * Ls + lens[b])
+            one = api.KV4Cache(*(t[b:b + 1] for t in ch.kv4[0]))
+            K, V = api.bitnet_kv4_read(one, 1, n, 0)
+            k, v = (host(t).reshape(n, kv, d).transpose(1, 0, 2) for t in (K, V))
+            at = pos[b] + np.arange(lens[b])
+            kt = KO.turn_rows(host(ch.k)[sl].reshape(-1, kv, d), at, hadamard=True)
+            err = np.abs(k[:, pos[b]:].transpose(1, 0, 2) - kt)
+            assert np.all(err <= np.abs(kt).max(-1, keepdims=True) / 14 * 1.0001)
+            check(host(ch.att)[sl].reshape(-1, 16, d), host(ch.q)[sl].reshape(-1, 16, d), k, v, at, 0, F32, 20, 2)
+
+
+def test_a_captured_chain_replays_at_other_positions():
+    rng = np.random.default_rng(92)
+    B, T, kv = 2, 96, 4
+    ch, eager = _chain(rng, B, (1, 1), T, kv, n_layers=2, hadamard=False)
+    x = torch.from_numpy(wl.gaussian(rng, (B, 2048))).cuda()
+    pos, lens = ints([0, 0]), ints([1, 1])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        ch.forward(x, stream=s, pos=pos, lens=lens)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            out = ch.forward(x, stream=s, pos=pos, lens=lens)
+    torch.cuda.current_stream().wait_stream(s)
+    for a, b in zip(ch.kv4, eager.kv4):
+        for t, u in zip(a, b):
+            u.copy_(t)
+    for at, n in (([1, 1], [1, 1]), ([2, 2], [1, 0]), ([3, 2], [1, 1]), ([90, 40], [1, 1])):
+        x.copy_(torch.from_numpy(wl.gaussian(rng, (B, 2048))))
+        pos.copy_(ints(at))
+        lens.copy_(ints(n))
+        graph.replay()
+        want = eager.forward(x, pos=ints(at), lens=ints(n))
+        real = torch.tensor(n, device="cuda") > 0
+        assert torch.equal(out[real], want[real])
+        for a, b in zip(ch.kv4, eager.kv4):
+            for t, u in zip(a, b):
+                assert torch.equal(t, u)
