@@ -82,6 +82,8 @@ _SIGNATURES = {
                                     [ctypes.c_size_t, ctypes.c_int, _c_void_p]),
     "bitnet_kv4_attention_workspace_size": (ctypes.c_size_t, [ctypes.c_int] + [_i64] * 2 + [ctypes.c_int] * 3 + [_i64] * 4 +
                                             [ctypes.c_int]),
+    "bitnet_kv4_attention_launches": (ctypes.c_int, [ctypes.c_int] + [_i64] * 2 + [ctypes.c_int] * 3 + [_i64] * 4 +
+                                      [ctypes.c_int]),
     "bitnet_device_error": (ctypes.c_int, [ctypes.POINTER(ctypes.c_int)]),
     "bitnet_measure_i8_mma": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, _c_void_p, _c_void_p,
                                              _c_void_p]),
@@ -544,6 +546,19 @@ def bitnet_kv4_attention_workspace_size(dtype, B: int, L: int, heads: int, kv_he
                                                          t_max, kernel))
 
 
+def bitnet_kv4_attention_launches(dtype, B: int, L: int, heads: int, kv_heads: int, head_dim: int, T_cap: int,
+                                  window: int = 0, sinks: int = 0, t_max: int = 0, kernel: int = 0) -> int:
+    """Kernels that bitnet_kv4_attention launches for these arguments (0: none)."""
+    code = {torch.float32: BITNET_F32, torch.bfloat16: BITNET_BF16}[dtype]
+    return int(lib().bitnet_kv4_attention_launches(code, B, L, heads, kv_heads, head_dim, T_cap, window, sinks, t_max,
+                                                   kernel))
+
+
+def _position_bound(T: int, t0: int, L: int, pos, t_max) -> int:
+    """The bound on positions that an attention call plans for."""
+    return min(T, (t0 + L if pos is None else T) if t_max is None else t_max)
+
+
 def bitnet_kv4_attention(Q: torch.Tensor, cache: KV4Cache, B: int, L: int, t0: int, heads: int, window: int = 0,
                          sinks: int = 0, t_max: int | None = None, pos=None, lens=None, A=None, workspace=None,
                          stream=None, kernel: int = 0):
@@ -559,7 +574,7 @@ def bitnet_kv4_attention(Q: torch.Tensor, cache: KV4Cache, B: int, L: int, t0: i
         raise ValueError("Q must be a contiguous CUDA tensor")
     kv, T, d, held = _cache_args(cache, B, dev)
     shape = (B * L, heads * d)
-    t_max = min(T, (t0 + L if pos is None else T) if t_max is None else t_max)
+    t_max = _position_bound(T, t0, L, pos, t_max)
     if A is None:
         A = _empty(shape, Q.dtype, dev, stream, zero=lens is not None)
     code = _dtype_code(Q)

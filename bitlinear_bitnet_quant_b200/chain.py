@@ -168,10 +168,20 @@ class BitLinearChain:
     # from the second layer on the first, with the residual add folded in), 4
     # linear launches (Q/K/V in one, O, up/gate in one, down), 2 Hadamard
     # quantisers (one with the gated unit folded in); one residual add after
-    # the last layer
+    # the last layer.  With attention the append and the attention's kernels: one,
+    # or over a 4-bit cache what the library launches for the last forward's step
     @property
     def launches(self) -> int:
-        return (8 if self.attention is None else 10) * len(self.layers) + 1
+        attention = 0
+        if self.attention is not None:
+            attention = 2
+            if self.kv_bits == 4 and self.layers:
+                B, L, cache = self.attention["B"], self.attention["L"], self.kv4[0].kc
+                T, d = cache.shape[2], 2 * cache.shape[3]
+                attention = 1 + api.bitnet_kv4_attention_launches(
+                    torch.float32, B, L, self.heads, self.kv_heads, d, T, self.window, self.sinks,
+                    api._position_bound(T, self.t0, L, self.pos, self.t_max))
+        return (8 + attention) * len(self.layers) + 1
 
     def packed_bytes(self) -> int:
         return sum(pk.numel() for w in self.layers for pk, _ in w.values())

@@ -51,6 +51,7 @@ bool kv4_prefill_applies(const KvStep& s, const AttnArgs& a, int bf16);
 size_t kv4_prefill_workspace(const KvStep& s, const AttnArgs& a, int bf16, int d);
 cudaError_t run_kv4_prefill(const KvStep& s, const AttnArgs& a, int bf16, int d, void* ws, size_t ws_bytes,
                             cudaStream_t st);
+int kv4_prefill_launches(const KvStep& s, const AttnArgs& a, int bf16, int d);
 size_t kv4_decode_workspace(const KvStep& s, const AttnArgs& a, int d);
 cudaError_t run_kv4_decode(const KvStep& s, const AttnArgs& a, int bf16, int d, void* ws, cudaStream_t st);
 }  // namespace bitnet
@@ -574,6 +575,20 @@ size_t bitnet_kv4_attention_workspace_size(int dtype, int64_t B, int64_t L, int 
   if (t_max > 0) s.limit = (int)t_max;
   const bitnet::AttnArgs a = kv4_attention_args(heads, kv_heads, window, sinks);
   return B == 0 || L == 0 ? 0 : kv4_workspace(s, a, dtype, head_dim, kernel);
+}
+
+int bitnet_kv4_attention_launches(int dtype, int64_t B, int64_t L, int heads, int kv_heads, int head_dim,
+                                  int64_t T_cap, int64_t window, int64_t sinks, int64_t t_max, int kernel) {
+  if (kernel < 0 || kernel > 2) return 0;
+  const int32_t any = 0;                                  // positions may come from the device
+  if (kv4_attention_shape(dtype, B, L, 0, &any, heads, kv_heads, head_dim, T_cap, window, sinks, t_max) != BITNET_OK)
+    return 0;
+  if (B == 0 || L == 0) return 0;
+  bitnet::KvStep s = kv_step(B, L, 0, nullptr, nullptr, T_cap);
+  if (t_max > 0) s.limit = (int)t_max;
+  const bitnet::AttnArgs a = kv4_attention_args(heads, kv_heads, window, sinks);
+  if (kv4_many_queries(s, a, dtype, kernel)) return bitnet::kv4_prefill_launches(s, a, dtype == BITNET_BF16, head_dim);
+  return bitnet::kv4_decode_workspace(s, a, head_dim) > 0 ? 2 : 1;         // with parts, the merge
 }
 
 int bitnet_kv4_attention_kernel(const void* Q, int dtype, const uint8_t* Kc, const float* Ks, const uint8_t* Vc,

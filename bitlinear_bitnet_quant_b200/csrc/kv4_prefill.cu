@@ -1048,6 +1048,17 @@ size_t kv4_prefill_workspace(const KvStep& s, const AttnArgs& a, int bf16, int d
   turn = turn < 1 ? 1 : (turn < heads ? turn : heads);
   return (size_t)(turn * head);
 }
+// Heads of a turn in a workspace of `bytes` (at most a grid dimension).
+static int kp_turn(const KvStep& s, const AttnArgs& a, int bf16, int d, size_t bytes) {
+  const int64_t fit = (int64_t)bytes / kp_head_bytes(s, a, bf16, d), heads = (int64_t)a.kv_heads * s.B;
+  const int64_t most = heads < 65535 ? heads : 65535;
+  return (int)(fit < most ? fit : most);
+}
+// Kernels of a call with a workspace of the size above: the expansion and the attention, a turn.
+int kv4_prefill_launches(const KvStep& s, const AttnArgs& a, int bf16, int d) {
+  const int turn = kp_turn(s, a, bf16, d, kv4_prefill_workspace(s, a, bf16, d));
+  return 2 * ((a.kv_heads * s.B + turn - 1) / turn);
+}
 
 template <int D, bool EXACT>
 static cudaError_t launch_prefill(const KvStep& s, const AttnArgs& a, uint8_t* ws, size_t ws_bytes, cudaStream_t st) {
@@ -1058,9 +1069,7 @@ static cudaError_t launch_prefill(const KvStep& s, const AttnArgs& a, uint8_t* w
   if (e != cudaSuccess) return e;
   const int row_tiles = (int)(((int64_t)s.L * (a.heads / a.kv_heads) + ROWS - 1) / ROWS);
   const int slots = (int)kp_slots(s, a), heads = a.kv_heads * s.B;
-  const int64_t fit = (int64_t)ws_bytes / kp_head_bytes(s, a, !EXACT, D);
-  const int most = heads < 65535 ? heads : 65535;            // a grid dimension
-  const int turn = (int)(fit < most ? fit : most);
+  const int turn = kp_turn(s, a, !EXACT, D, ws_bytes);
   if (turn < 1) return cudaErrorInvalidValue;
   float* factors = reinterpret_cast<float*>(ws + (int64_t)turn * slots * KpTile<D>::PAIR);
   for (int head0 = 0; head0 < heads; head0 += turn) {

@@ -445,6 +445,9 @@ BITNET_API int bitnet_kv4_attention_kernel(const void* Q, int dtype, const uint8
                                            int head_dim, int64_t T_cap, int64_t window, int64_t sinks, int64_t t_max,
                                            void* A, void* workspace, size_t workspace_bytes, int kernel,
                                            void* stream);
+/* Kernels that such a call launches with a workspace of the size above (0: a no-op or refused). */
+BITNET_API int bitnet_kv4_attention_launches(int dtype, int64_t B, int64_t L, int heads, int kv_heads, int head_dim,
+                                             int64_t T_cap, int64_t window, int64_t sinks, int64_t t_max, int kernel);
 
 /*
  * Reads and clears the library's device-side error flag on the current

@@ -380,3 +380,30 @@ def test_a_captured_chain_replays_at_other_positions():
         for a, b in zip(ch.kv4, eager.kv4):
             for t, u in zip(a, b):
                 assert torch.equal(t, u)
+
+
+def _kernels_of(call):
+    """Kernels that call() enqueues, counted in a capture of it."""
+    from cuda.bindings import driver
+    call()
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(graph):
+        call()
+    raw = driver.CUgraph(graph.raw_cuda_graph())
+    err, _, count = driver.cuGraphGetNodes(raw)
+    assert int(err) == 0
+    err, nodes, count = driver.cuGraphGetNodes(raw, count)
+    assert int(err) == 0 and len(nodes) == count
+    kinds = [driver.cuGraphNodeGetType(n) for n in nodes]
+    assert all(int(e) == 0 for e, _ in kinds)
+    return sum(kind == driver.CUgraphNodeType.CU_GRAPH_NODE_TYPE_KERNEL for _, kind in kinds)
+
+
+@pytest.mark.parametrize("L,T,t0,kw", [(1, 64, 20, {}), (1, 4096, 4000, {}), (512, 512, 0, {}),
+                                       (1, 4096, 0, dict(pos=[5])), (1, 4096, 0, dict(pos=[5], t_max=40))])
+def test_launches_counts_the_kernels(L, T, t0, kw):
+    rng = np.random.default_rng(93)
+    ch, = _chain(rng, 1, (L,), T, 16, n_layers=2)
+    x = torch.from_numpy(wl.gaussian(rng, (L, 2048))).cuda()
+    kw = dict(kw, pos=ints(kw["pos"])) if "pos" in kw else kw
+    assert _kernels_of(lambda: ch.forward(x, t0=t0, **kw)) == ch.launches
