@@ -278,16 +278,14 @@ struct KpRows {
 // 2^x of a pair on the multiply-add units: x = n + r with r in [-1/2, 1/2] by adding
 // 1.5 * 2^23, a cubic for 2^r (relative error 1e-4, a fifth of the fp16 rounding that
 // follows), and n into the exponent.  x below -125 counts as -125 (2^-125 rounds to
-// zero in fp16), x above 127 as 127: a score far above the maximum so far must show in
-// the weights' sum, and 2^n with n > 127 would run into the sign.  NaN comes out as a
-// large number.  (The upper bound costs 0.7 % of 8192 causal tokens.)
-BN_DEV void exp2_pair(uint64_t x, float& e0, float& e1) {
+// zero in fp16).  2^n with n > 127 runs into the sign and means nothing, nor does NaN:
+// the caller finds both in `high`, the largest n + 1.5 * 2^23.  (Without that a key far
+// above the maximum so far lost its weight; it costs 0.7 % of 8192 causal tokens.)
+BN_DEV void exp2_pair(uint64_t x, float& e0, float& e1, float& high) {
   float a, b;
   unpack_f2(x, a, b);
   asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(-125.f));
   asm("max.NaN.f32 %0, %0, %1;" : "+f"(b) : "f"(-125.f));
-  asm("min.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(127.f));
-  asm("min.NaN.f32 %0, %0, %1;" : "+f"(b) : "f"(127.f));
   const uint64_t v = pack_f2(a, b);
   const uint64_t big = pack_f2(12582912.f, 12582912.f), nbig = pack_f2(-12582912.f, -12582912.f);
   const uint64_t t = add_f2(v, big);
@@ -298,23 +296,26 @@ BN_DEV void exp2_pair(uint64_t x, float& e0, float& e1) {
   q = fma_f2(q, r, pack_f2(EXP2_C0, EXP2_C0));
   float t0, t1, q0, q1;
   unpack_f2(t, t0, t1);
+  high = max3_nan(high, t0, t1);
   unpack_f2(q, q0, q1);
   e0 = __uint_as_float(__float_as_uint(q0) + (__float_as_uint(t0) << 23));
   e1 = __uint_as_float(__float_as_uint(q1) + (__float_as_uint(t1) << 23));
 }
 
 // The weights of a tile's keys for one row, as fp16 pairs, for exponents x f + ref, and
-// their sum.  Every KP_POLY-th pair's exponentials come from the multiply-add units: the
-// special-function units alone would take 2048 cycles a tile.
+// their sum (infinite where one is not finite or too large for exp2_pair).  Every
+// KP_POLY-th pair's exponentials come from the multiply-add units: the special-function
+// units alone would take 2048 cycles a tile.
 BN_DEV void kp_weights(const float (&x)[KP_KT], float f, float ref, uint32_t (&w)[KP_KT / 2], float& sum) {
   const uint64_t f2 = pack_f2(f, f), ref2 = pack_f2(ref, ref);
   uint64_t s2[4] = {0, 0, 0, 0};
+  float high[2] = {0.f, 0.f};
 #pragma unroll
   for (int c = 0; c < KP_KT / 2; ++c) {
     float e0, e1;
     const uint64_t y = fma_f2(pack_f2(x[2 * c], x[2 * c + 1]), f2, ref2);
     if (c % KP_POLY == KP_POLY - 1) {
-      exp2_pair(y, e0, e1);
+      exp2_pair(y, e0, e1, high[(c / KP_POLY) & 1]);
     } else {
       unpack_f2(y, e0, e1);
       e0 = ex2(e0);
@@ -325,7 +326,7 @@ BN_DEV void kp_weights(const float (&x)[KP_KT], float f, float ref, uint32_t (&w
   }
   float s0, s1;
   unpack_f2(add_f2(add_f2(s2[0], s2[1]), add_f2(s2[2], s2[3])), s0, s1);
-  sum = s0 + s1;
+  sum = max_nan(high[0], high[1]) <= 12582912.f + 127.f ? s0 + s1 : INFINITY;
 }
 // The largest score of a row, NaN where one is.
 BN_DEV float kp_top(const float (&x)[KP_KT]) {
