@@ -540,7 +540,8 @@ def bitnet_kv4_read(cache: KV4Cache, B: int, L: int, t0: int, pos=None, lens=Non
 
 def bitnet_kv4_attention_workspace_size(dtype, B: int, L: int, heads: int, kv_heads: int, head_dim: int, T_cap: int,
                                         window: int = 0, sinks: int = 0, t_max: int = 0, kernel: int = 0) -> int:
-    """Bytes of workspace bitnet_kv4_attention needs for these arguments (0: none)."""
+    """Bytes of workspace bitnet_kv4_attention needs for these arguments (0: none).  t_max as the
+    call gets it, 0 being T_cap; a call that gets none takes t0 + L without pos, else T_cap."""
     code = {torch.float32: BITNET_F32, torch.bfloat16: BITNET_BF16}[dtype]
     return int(lib().bitnet_kv4_attention_workspace_size(code, B, L, heads, kv_heads, head_dim, T_cap, window, sinks,
                                                          t_max, kernel))

@@ -55,7 +55,8 @@ class BitLinearChain:
                  key heads before the keys are held in 4 bits;
       kv_heads   (kv_bits 4; default heads) key heads, each shared by
                  heads / kv_heads query heads;
-      window, sinks  (kv_bits 4) sliding window and first tokens that stay visible."""
+      window, sinks  (kv_bits 4) sliding window and first tokens that stay visible;
+                 keys behind the window keep their place, positions stay below T_cap."""
 
     def __init__(self, layers: list, M: int, hidden: int, ffn: int, device, eps: float = 1e-6, attention=None):
         self.layers = layers

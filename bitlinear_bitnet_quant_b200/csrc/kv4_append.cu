@@ -19,7 +19,7 @@
 //
 // What bounds it: without the Hadamard transform memory (8000 bf16 tokens of 32 + 8 + 8
 // heads with norm into fp32 caches, 61 us, 74 % of a copy's rate); with it the instruction
-// issue (73 % of the cycles), half of a query's instructions being the transform's exchanges
+// issue (69 % of the cycles), half of a query's instructions being the transform's exchanges
 // between lanes (32768 such tokens into the 4-bit cache, 215 us, 3.3 TB/s).  Every input is
 // read once and every output written once.
 // 8 values a lane (one 16-byte load of bf16 rows): 16 lanes (d = 128) or 8 (d = 64)
@@ -319,7 +319,8 @@ append_kernel(const KvStep s, const AppendArgs a, const __grid_constant__ RopeTa
 // ---------------------------------------------------------------------------
 // 4-bit rows back to values: a thread writes 16 bytes of a key row and of the value
 // row (half a word's codes as fp32, a word's as bf16), so that a warp's stores are one
-// run of memory.  Bound by the stores: 32768 tokens of 8 heads to fp32 in 70 us, 4.3 TB/s.
+// run of memory.  Bound by the instructions that take the codes apart (they issue in two
+// thirds of the cycles): 32768 tokens of 8 heads to fp32 in 70 us, 4.3 TB/s.
 // ---------------------------------------------------------------------------
 BN_DEV float code_value(uint32_t w, int i, float step) {   // code i of a word
   const int c = (int)(w << (28 - 4 * (i >> 1) - 16 * (i & 1))) >> 28;

@@ -28,11 +28,11 @@ namespace bitnet {
 // head, times a few tokens) cost one product.  A warp takes every (warps)-th tile
 // of 32 keys through its own ring of asynchronous copies; scores, weights and the
 // output stay in its registers.  Taking the codes apart costs more than reading them
-// (16 bf16 sequences of 2048 to 32768 keys, 32 over 8 heads: 114 us, of which the memory
-// needs 46); a single short sequence is latency (513 keys, 16 heads: 7 us in a graph).
-// The warps' partial softmaxes are merged in shared memory; where several blocks share a
-// row tile's keys, over distributed shared memory of a cluster, or (many blocks a row
-// tile) through the workspace by a second kernel.
+// (16 bf16 sequences of 2048 to 32768 keys, 32 over 8 heads: 113 us, of which the memory
+// needs 46), by too few warps to fill the issue slots (59 %); a single short sequence is
+// latency (513 keys, 16 heads: 7 us in a graph).  The warps' partial softmaxes are merged
+// in shared memory; where several blocks share a row tile's keys, over distributed shared
+// memory of a cluster, or (many blocks a row tile) through the workspace by a second kernel.
 // ---------------------------------------------------------------------------
 constexpr int KD_WARPS = 4;
 constexpr int KD_STAGES = 3;

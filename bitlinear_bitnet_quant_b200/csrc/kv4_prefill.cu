@@ -47,11 +47,10 @@ BN_DEV bool elect_one() {
   return p != 0;
 }
 
-// Instruction descriptor of kind::f16: fp32 accumulator, fp16 or bf16 operands, A
-// K-major, B K-major or (b_mn) with its N dimension contiguous.
-__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool bf16, bool b_mn) {
-  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? (1u << 16) : 0u) | ((uint32_t)(N >> 3) << 17) |
-         ((uint32_t)(M >> 4) << 24);
+// Instruction descriptor of kind::f16: fp32 accumulator, fp16 operands, A K-major, B
+// K-major or (b_mn) with its N dimension contiguous.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
+  return (1u << 4) | (b_mn ? (1u << 16) : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 // Shared-memory descriptors (128-byte swizzle, groups of 8 rows 1024 bytes apart) as a
 // low word that a product's offset is added to and a constant high word: the warp that
@@ -109,8 +108,8 @@ BN_DEV KpSeen kp_seen(const KvStep& s, int b) {
 // by memory (reads D + 8 bytes a key and head, writes 4 D): 8192 keys of 8 heads in 15 us,
 // 3 % of the attention they are for.
 // ---------------------------------------------------------------------------
-// EXACT (fp32 rows): the images hold the codes themselves, and for every key the factors
-// of KpKey are written instead of the tile's.
+// EXACT (fp32 rows): the images hold the codes themselves, and every key's four factors
+// (KP_KEY_FLOATS a tile) are written instead of the tile's.
 template <int D, bool EXACT>
 __global__ void __launch_bounds__(256)
 kv4_expand_kernel(const KvStep s, const AttnArgs a, int head0, int slots, float scale_log2e, uint8_t* images,
@@ -228,8 +227,9 @@ BN_DEV bool kp_padding(const KvStep& s, const AttnArgs& a, int head0, int heads_
 // and only where their sum passes what one weight may be in fp16 (or a row sees its first
 // key) is the tile's maximum found, the output in tensor memory rescaled and the weights
 // computed once more.  (Finding every tile's maximum: 522 us for 8192 causal tokens of
-// 8 x 4 heads, so 499: 1.1 PFLOP/s, 67 % of a library product's rate, the rest the
-// softmax's instructions and the filling and draining of 7 blocks an SM.)
+// 8 x 4 heads, so 504: 1.1 PFLOP/s, 67 % of a library product's rate, for a call alone with a
+// cold L2, and 575 us among others, where the clock is lower.  The rest are the softmax's
+// instructions and the filling and draining of 7 blocks an SM.)
 // ---------------------------------------------------------------------------
 constexpr int KP_THREADS = 320;                      // streams: warps 0-3 and 4-7; products: warp 8; copies: warp 9
 
@@ -607,7 +607,7 @@ kv4_prefill_kernel(const KvStep s, const AttnArgs a, int head0, int heads_here, 
   } else {
     if (warp == 8 && tiles.count > 0) {
       // ---------------------------------------------- products
-      constexpr uint32_t ID_S = idesc_f16(128, KP_KT, false, false), ID_O = idesc_f16(128, D, false, true);
+      constexpr uint32_t ID_S = idesc_f16(128, KP_KT, false), ID_O = idesc_f16(128, D, true);
       bool ok = kp_wait(&q_full, 0, DEV_ERR_TIMEOUT_A);
       const uint32_t qd = desc_lo(smem_u32(sm + M::Q));
       const uint32_t kd = desc_lo(smem_u32(sm + M::K)), vd = desc_lo(smem_u32(sm + M::V));
@@ -898,7 +898,7 @@ kv4_prefill_f32_kernel(const KvStep s, const AttnArgs a, int head0, int heads_he
     }
   } else if (warp == 12 && tiles.count > 0) {
     // ------------------------------------------------ products
-    constexpr uint32_t ID_S = idesc_f16(128, KP_KT, false, false), ID_O = idesc_f16(128, D, false, true);
+    constexpr uint32_t ID_S = idesc_f16(128, KP_KT, false), ID_O = idesc_f16(128, D, true);
     ok = kp_wait(&q_full, 0, DEV_ERR_TIMEOUT_A);
     const uint32_t qd = desc_lo(smem_u32(sm + M::Q));
     const uint32_t kd = desc_lo(smem_u32(sm + M::K)), vd = desc_lo(smem_u32(sm + M::V));

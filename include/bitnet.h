@@ -354,8 +354,9 @@ BITNET_API int bitnet_attention(const float* Q, const float* Kc, const float* Vc
  *   4 bits    t = fp32(y);  s = 7 / max(max|t|, 1e-5);  code = clamp(rint(t * s),
  *             -8, 7);  step = 1 / s.  The row stands for code * step.
  *   Keys of the 4-bit cache are computed in fp64 up to t, queries and fp32 caches
- *   in fp32 (angles in fp64).  A row with a NaN or an infinity gets the step NaN: it
- *   reads back as NaN and makes the queries that see it NaN.
+ *   in fp32 (angles in fp64; a norm's sum of squares past the range of fp32 gives zeros
+ *   there).  A row with a NaN or an infinity gets the step NaN: it reads back as NaN and
+ *   makes the queries that see it NaN.
  * 4-bit caches: codes Kc, Vc [B][kv_heads][T_cap][d/2] bytes, steps Ks, Vs
  *   [B][kv_heads][T_cap] fp32, T_cap % 16 == 0.  Of each 8 codes of a row (one
  *   little-endian 32-bit word), code 2j + i (i = 0, 1) sits at bits 4j + 16i, two's
@@ -367,7 +368,9 @@ BITNET_API int bitnet_attention(const float* Q, const float* Kc, const float* Vc
  *   fp32 receives the turned queries (it may be Q itself where x_dtype is
  *   BITNET_F32 and ldq == heads*d); Kc, Vc [B][T_cap][kv_heads*d] fp32 the turned
  *   keys and the values.  gamma_q, gamma_k: [d] fp32 or NULL (ones).  rot_dim: even,
- *   0 .. d.  base > 1.
+ *   0 .. d.  base > 1.  (bitnet_attention reads such caches where kv_heads == heads,
+ *   head_dim is 128 and every sequence stands at the same position; shared key heads,
+ *   ragged positions and heads of 64 have their attention over the 4-bit cache.)
  */
 BITNET_API int bitnet_qk_norm_rope_append(const void* Q, const void* K, const void* V, int x_dtype, int64_t ldq,
                                           int64_t ldk, int64_t ldv, int64_t B, int64_t L, int64_t t0,
@@ -412,14 +415,16 @@ BITNET_API int bitnet_kv4_read(const uint8_t* Kc, const float* Ks, const uint8_t
  *   smallest weigh nothing.  (Where a row's largest |q| times a step that it sees passes
  *   2^126, a product of zero may count as NaN.)  No other row is touched by that.
  * Q, A   : [B*L][heads*d] in dtype (A may be Q itself).
- * window : 0 (every key) or the number of keys of the window; sinks >= 0.
+ * window : 0 (every key) or the number of keys of the window; sinks >= 0.  Keys behind
+ *          the window are not read, but the cache is no ring: positions stay below T_cap.
  * t_max  : a bound on the positions in use plus one, 1 .. T_cap, or 0 (T_cap): a
  *          query at or past it counts as outside the cache.  The work is split, and
  *          the workspace sized, for it.
  * workspace: device scratch, 16-byte aligned, of at least
  *          bitnet_kv4_attention_workspace_size bytes for the same arguments (0: not
  *          read; up to 256 MB, or one key head's share of the cache in fp16 where that
- *          is more), overwritten.  Two calls that may run at the same
+ *          is more), overwritten.  The size follows t_max, and not always upwards: a
+ *          workspace serves calls of the t_max that it was sized for.  Two calls that may run at the same
  *          time, captured ones among them, need one each.
  * fp32 softmax; products with fp16 operands: fp32 rows against exact codes, queries
  * and weights to 22 bits; bf16 rows exactly, weights (and, for many queries, code *
